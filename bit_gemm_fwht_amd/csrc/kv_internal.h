@@ -1,0 +1,63 @@
+// The paged 8-bit key / value cache as the kernels see it, and the launchers behind the C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace bgf {
+
+// Cache and batch of one call (layouts in include/fp4.h).
+struct KvView {
+    uint8_t* kc;
+    uint8_t* vc;
+    uint8_t* ks;
+    uint8_t* vs;
+    int64_t pages;
+    int H, D, P, pshift;  // kv heads, head dim, tokens of a page and its log2
+    const int32_t* cu;
+    const int32_t* ctx;
+    const int32_t* table;
+    int64_t table_ld;
+    int S, W;  // sequences, pages of a table row
+    int T;     // rows of the batch
+};
+
+// Rows to or from the cache: k and v [T, H, D], strides in elements.
+struct KvRowsArgs {
+    KvView c;
+    const void* k;
+    const void* v;
+    int64_t ldk, ldk_head, ldv, ldv_head;
+    int ceil_rule;
+};
+
+struct KvAttnArgs {
+    KvView c;
+    const void* q;
+    void* out;
+    float* lse;
+    int64_t ldq, ldq_head, ldo, ldo_head;
+    int Hq, G;
+    float scale_log2;  // scale * log2(e)
+    int causal, window;
+    int chunk;         // keys of one split, a multiple of 64
+    int Z;             // splits of the launch
+    unsigned slots;    // row tiles of the launch (an upper bound of those that have rows)
+    float* part_o;     // [Z][H][slots][rows of a tile][D] unnormalised outputs
+    float* part_ml;    // [Z][H][slots][rows of a tile][2] maximum (log2 units) and sum
+};
+
+hipError_t launch_kv_append(const KvRowsArgs& a, int dtype, hipStream_t s);
+hipError_t launch_kv_read(const KvRowsArgs& a, int dtype, hipStream_t s);
+
+// How an attention call is cut into workgroups; the same for the size query and the launch.
+struct KvAttnPlan {
+    unsigned slots;
+    int rows;    // rows of a tile
+    int Z, chunk;
+    int64_t ws;  // bytes of workspace
+};
+KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int max_tokens, int max_context);
+hipError_t launch_kv_attention(KvAttnArgs a, const KvAttnPlan& p, int dtype, void* ws, hipStream_t s);
+
+}  // namespace bgf

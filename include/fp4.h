@@ -14,7 +14,9 @@
  *    E4M3 block scale and an fp32 tensor scale, and the adaptive 4/6 choice ("Four Over Six: More
  *    Accurate NVFP4 Quantization with Adaptive Block Scaling", methodology);
  *  - the GEMM on the quantized operands, one call, fp32 accumulation (the QuTLASS kernel list
- *    of the Quartet notes: 4-bit GEMM, online quantization of the output).
+ *    of the Quartet notes: 4-bit GEMM, online quantization of the output);
+ *  - the key / value cache in the same E4M3 + E8M0 blocks: quantized as it is written, read back, and
+ *    attention over it (own section at the end).
  *
  * Conventions for every entry point:
  *  - Pointers named x, y, codes, scales, tensor_scale, C and workspace are DEVICE pointers
@@ -281,6 +283,102 @@ int fp4_transpose_2d(const void* codes, const void* scales, int64_t rows, int64_
  * out_codes 16-byte aligned, scales 2-byte aligned; outputs must not alias the inputs. */
 int fp4_nvfp4_to_mxfp8(const void* codes, const void* scales, int64_t rows, int64_t cols, void* out_codes,
                        void* out_scales, void* stream);
+
+/* ---- The key / value cache in 8 bits: written, read back, attended over -------------------------
+ *
+ * The cache is paged: a page holds page_tokens consecutive tokens of one sequence for every kv head.
+ * Elements are E4M3 and every block (one page's tokens of one head) has one E8M0 scale for K and one
+ * for V (code e + 127): the block scales of this library with a block of page_tokens x head_dim.
+ *   k_codes  [pages, kv_heads, page_tokens, head_dim]   a token's row contiguous
+ *   v_codes  [pages, kv_heads, head_dim, page_tokens]   transposed in the page: a channel's tokens
+ *            contiguous, the order in which the product of probabilities and values reads them
+ *   k_scales, v_scales [pages, kv_heads]
+ * page_tokens is 16, 32, 64 or 128; head_dim a multiple of 16 up to 256; codes 16-byte aligned. Every
+ * buffer is contiguous. The place of an element is computed in 64 bits.
+ *
+ * A batch says how the rows of q, k and v belong to sequences and where those live (device int32):
+ *   cu_tokens [seqs + 1]   rows cu_tokens[s] .. cu_tokens[s + 1] - 1 are sequence s's (a sequence may
+ *                          have none); ascending from 0 to tokens
+ *   context   [seqs]       the sequence's tokens in the cache, the batch's own included: row i of a
+ *                          sequence with n rows is its token context - n + i (no token if negative)
+ *   table     [seqs, table_pages], row pitch table_ld: the sequence's pages in order; token t is in
+ *                          page table[s][t / page_tokens] at t % page_tokens
+ * The kernels check these values, which the host does not see: rows outside [0, tokens), tokens past
+ * table_pages * page_tokens and pages outside [0, pages) are not touched; in attention such keys are
+ * masked. max_tokens and max_context, the largest number of rows and the largest context of any
+ * sequence, are hints (0: not known): they choose how work is split and never change which result is
+ * meant. tokens == 0 queues nothing and returns FP4_OK.
+ * Row strides of q, k, v and the outputs are in elements, one for tokens (ld) and one for heads
+ * (ld_head), each a multiple of 16 bytes, the rows themselves contiguous and 16-byte aligned (e.g.
+ * slices of one fused projection). */
+typedef struct fp4_kv_cache {
+    void* k_codes;
+    void* v_codes;
+    void* k_scales;
+    void* v_scales;
+    int64_t pages;
+    int32_t kv_heads;
+    int32_t page_tokens;
+    int32_t head_dim;
+} fp4_kv_cache;
+
+typedef struct fp4_kv_batch {
+    const int32_t* cu_tokens;
+    const int32_t* context;
+    const int32_t* table;
+    int64_t tokens;
+    int64_t table_ld;
+    int32_t seqs;
+    int32_t table_pages;
+    int32_t max_tokens;
+    int32_t max_context;
+} fp4_kv_batch;
+
+/* Quantize k and v [tokens, kv_heads, head_dim] (fp32 or bf16) into the cache as they are written.
+ * Per block that receives tokens: amax = max |x| over the block's new tokens, e the E8M0 exponent of
+ * amax for E4M3 (scale_mode FP4_SCALE_E8M0_FLOOR or _CEIL); where the block already holds older tokens
+ * of the sequence, e = max(e, its exponent) and, if that grew, the older codes c become
+ * E4M3(c * 2^(old - e)), nearest even (exact except where an element falls below E4M3's normal range).
+ * New elements are E4M3(x * 2^-e), nearest even, saturating. Places of the page that hold no token
+ * yet are left as they are. Writing the same tokens again gives the same cache. Two sequences of a
+ * batch must not write to one page. */
+int fp4_kv_append(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const void* k, int64_t ldk, int64_t ldk_head,
+                  const void* v, int64_t ldv, int64_t ldv_head, int32_t dtype, int32_t scale_mode, void* stream);
+
+/* Read tokens back: row i of a sequence with n rows becomes the K and V of its token context - n + i
+ * (n = context for the whole of it), k and v [tokens, kv_heads, head_dim] fp32 or bf16 (exact in both
+ * while c * 2^e is in their normal range). Rows with no token in the cache are left as they are. */
+int fp4_kv_read(const fp4_kv_cache* cache, const fp4_kv_batch* batch, void* k, int64_t ldk, int64_t ldk_head,
+                void* v, int64_t ldv, int64_t ldv_head, int32_t dtype, void* stream);
+
+/* Attention over the cache. q and out [tokens, q_heads, head_dim] of one dtype (fp32 or bf16); q head
+ * h reads kv head h / (q_heads / kv_heads) (q_heads a multiple of kv_heads). For the query at position
+ * p (its row's token, above) key j is allowed iff 0 <= j < context, (causal != 0) j <= p and
+ * (window > 0) j > p - window, and
+ *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q.k_j),  lse = ln sum_j w_j
+ * over the allowed keys; a row with none gives zeros and lse = -inf. What the cache holds in places
+ * that are not allowed for any query of a sequence (past its context, pages before every window)
+ * is never used, whatever its bits. Scores, softmax statistics and sums are fp32; with fp32 q, q and
+ * the weights enter the matrix products as exact sums of three bf16, with bf16 q the weights as sums
+ * of two (2^-17 off at most; K and V enter exactly). Results do not depend on timing: no atomics.
+ * lse: fp32 [tokens, q_heads], contiguous, or NULL. workspace: at least
+ * fp4_kv_attention_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0; -1 for arguments
+ * that the call would reject); it holds the partial results of keys split over the chip. */
+typedef struct fp4_kv_attn {
+    const void* q;
+    void* out;
+    float* lse;
+    int64_t ldq, ldq_head;
+    int64_t ldo, ldo_head;
+    int32_t dtype;
+    int32_t q_heads;
+    int32_t causal;
+    int32_t window;
+    float scale;
+} fp4_kv_attn;
+int64_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv_attn* a);
+int fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv_attn* a, void* workspace,
+                     int64_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
