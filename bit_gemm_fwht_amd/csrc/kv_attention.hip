@@ -129,8 +129,14 @@ __device__ __forceinline__ void store_out4(void* out, int64_t at, f32x4 y) {
 // ---------------------------------------------------------------------------------------------
 constexpr int kRows = 16;
 
-template <int DT, int U>  // U: 64-channel pieces of a head
-__global__ __launch_bounds__(256) void k_kv_attn_rows(KvAttnArgs a) {
+// Waves a SIMD holds at once: as many as the registers of the variant allow without spills (a lane
+// holds 16 U of K and V each on their way, 16 U of o, 8 U (fp32: 24 U) of q).
+constexpr int rows_waves(int dt, int u) {
+    return dt == DT_BF16 ? (u == 1 ? 4 : u == 2 ? 3 : u == 3 ? 2 : 1) : (u == 1 ? 3 : u == 2 ? 2 : 1);
+}
+
+template <int DT, int U, bool FULL>  // U: 64-channel pieces of a head; FULL: the head fills them
+__global__ __launch_bounds__(256, rows_waves(DT, U)) void k_kv_attn_rows(KvAttnArgs a) {
     constexpr int NS = DT == DT_BF16 ? 1 : 3, NP = DT == DT_BF16 ? 2 : 3;  // bf16 a query and a weight take
     const KvView& c = a.c;
     const int h = blockIdx.y, z = blockIdx.z;
@@ -138,7 +144,7 @@ __global__ __launch_bounds__(256) void k_kv_attn_rows(KvAttnArgs a) {
     if (t.s < 0 || z >= t.splits) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int li = lane & 15, g = lane >> 4;
-    const int D = c.D, P = c.P;
+    const int D = FULL ? 64 * U : c.D, P = c.P;
 
     // this lane's query row
     const int r = t.r0 + li;
@@ -197,32 +203,39 @@ __global__ __launch_bounds__(256) void k_kv_attn_rows(KvAttnArgs a) {
     const int begin = (t.lo & ~63) + z * a.chunk;
     const int end = z == t.splits - 1 ? t.hi : min(t.hi, begin + a.chunk);
     const int gk = li >> 2;  // S^T row li of piece e is key 16 gk + 4 e + (li & 3) of the step
-    for (int kb = begin + 64 * wave; kb < end; kb += 256) {
-        // pages of the 16 keys this lane loads K for, and of the 16 it loads V for
+    // pages of the 16 keys this lane loads K for, and of the 16 it loads V for; the next step's are
+    // looked up while this step's K and V are on their way
+    const auto page_of = [&](int key) { return key < t.hi ? page_at(c, t.s, key >> c.pshift) : -1; };
+    int kb = begin + 64 * wave;
+    int pk_next = page_of(kb + 16 * gk), pv_next = page_of(kb + 16 * g);
+#pragma unroll 1
+    for (; kb < end; kb += 256) {
         const int tk = kb + 16 * gk, tv = kb + 16 * g;
-        const int pk = tk < t.hi ? page_at(c, t.s, tk >> c.pshift) : -1;
-        const int pv = tv < t.hi ? page_at(c, t.s, tv >> c.pshift) : -1;
+        const int pk = pk_next, pv = pv_next;
+        pk_next = page_of(tk + 256);
+        pv_next = page_of(tv + 256);
         u32x4 kraw[4][U], vraw[4 * U];
         const uint8_t* kp = c.kc + ((((int64_t)max(pk, 0) * c.H + h) << c.pshift) + (tk & (P - 1)) + (li & 3)) * D + 16 * g;
         const uint8_t* vp = c.vc + (((int64_t)max(pv, 0) * c.H + h) * D + li) * P + (tv & (P - 1));
+        // (loads are not conditional: a lane with nothing to load reads page 0 and is masked below, a
+        // piece past the head's channels is read from its start and not used)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                kraw[e][u] = (u32x4){0, 0, 0, 0};
-                if (pk >= 0 && 64 * u + 16 * g < D) kraw[e][u] = *reinterpret_cast<const u32x4*>(kp + 4 * e * D + 64 * u);
+                const bool in = FULL || 64 * u + 16 * g < D;
+                const u32x4 w = *reinterpret_cast<const u32x4*>(kp + 4 * e * D + (in ? 64 * u : -16 * g));
+                kraw[e][u] = in ? w : (u32x4){0, 0, 0, 0};
             }
 #pragma unroll
-        for (int i = 0; i < 4 * U; ++i) {
-            vraw[i] = (u32x4){0, 0, 0, 0};
-            if (pv >= 0 && 16 * i < D) vraw[i] = *reinterpret_cast<const u32x4*>(vp + 16 * i * P);
-        }
+        for (int i = 0; i < 4 * U; ++i) vraw[i] = *reinterpret_cast<const u32x4*>(vp + (FULL || 16 * i < D ? 16 * i * P : 0));
         const int64_t sb = (int64_t)max(pv, 0) * c.H + h;
         const float kscale = fminf(e8m0_value(c.ks[sb]) * a.scale_log2, 3.40282347e38f);
         const float vscale = e8m0_value(c.vs[sb]);
 
         // scores of this lane's row and keys kb + 16 g + 0 .. 15, in log2 units
         float s[16];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             f32x4 acc = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -248,7 +261,7 @@ __global__ __launch_bounds__(256) void k_kv_attn_rows(KvAttnArgs a) {
             // V where no row may attend is whatever memory held: made zero, as 0 * NaN is not 0
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int n1 = min(max(t.hi - tv - 4 * j, 0), 4), n0 = min(max(t.lo - tv - 4 * j, 0), 4);
+                const int n1 = pv < 0 ? 0 : min(max(t.hi - tv - 4 * j, 0), 4), n0 = min(max(t.lo - tv - 4 * j, 0), 4);
                 uint32_t keep = n1 == 4 ? 0xFFFFFFFFu : (1u << (8 * n1)) - 1u;
                 keep &= n0 == 4 ? 0u : 0xFFFFFFFFu << (8 * n0);
 #pragma unroll
@@ -256,6 +269,7 @@ __global__ __launch_bounds__(256) void k_kv_attn_rows(KvAttnArgs a) {
             }
         }
 
+        __builtin_amdgcn_sched_barrier(0);
         float mx = s[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
@@ -275,17 +289,16 @@ __global__ __launch_bounds__(256) void k_kv_attn_rows(KvAttnArgs a) {
             s[i] = __builtin_amdgcn_exp2f(s[i] - ms);
             l += s[i];
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             bf16x8 pf[NP];
             split8<NP>(s + 8 * w, pf);
 #pragma unroll
             for (int i = 0; i < 4 * U; ++i) {
-                if (16 * i < D) {
-                    const bf16x8 vf = cvt8(vraw[i][2 * w], vraw[i][2 * w + 1], vscale);
+                const bf16x8 vf = cvt8(vraw[i][2 * w], vraw[i][2 * w + 1], vscale);
 #pragma unroll
-                    for (int n = 0; n < NP; ++n) o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[n], o[i], 0, 0, 0);
-                }
+                for (int n = 0; n < NP; ++n) o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[n], o[i], 0, 0, 0);
             }
         }
     }
@@ -393,7 +406,9 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
 
 template <int DT, int U>
 static void launch_rows(const KvAttnArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((k_kv_attn_rows<DT, U>), dim3(a.slots, (unsigned)a.c.H, (unsigned)a.Z), dim3(256), 0, s, a);
+    const dim3 grid(a.slots, (unsigned)a.c.H, (unsigned)a.Z);
+    if (a.c.D == 64 * U) hipLaunchKernelGGL((k_kv_attn_rows<DT, U, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_kv_attn_rows<DT, U, false>), grid, dim3(256), 0, s, a);
 }
 
 template <int DT>
