@@ -105,7 +105,8 @@ int attn_args(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv
     a->ldo_head = t->ldo_head;
     a->Hq = t->q_heads;
     a->G = t->q_heads / cache->kv_heads;
-    a->scale_log2 = (float)((double)t->scale * 1.4426950408889634);
+    a->scale_log2 = (float)(std::fabs((double)t->scale) * 1.4426950408889634);
+    a->flip = t->scale < 0.0f;
     a->causal = t->causal != 0;
     a->window = t->window;
     *p = plan_kv_attention(a->c, t->q_heads, t->window, t->dtype, batch->max_tokens, batch->max_context);

@@ -38,13 +38,14 @@ struct KvAttnArgs {
     float* lse;
     int64_t ldq, ldq_head, ldo, ldo_head;
     int Hq, G;
-    float scale_log2;  // scale * log2(e)
+    float scale_log2;  // |scale| * log2(e)
+    int flip;          // scale < 0: q is negated
     int causal, window;
-    int chunk;         // keys of one split, a multiple of 64
-    int Z;             // splits of the launch
-    unsigned slots;    // row tiles of the launch (an upper bound of those that have rows)
-    float* part_o;     // [Z][H][slots][rows of a tile][D] unnormalised outputs
-    float* part_ml;    // [Z][H][slots][rows of a tile][2] maximum (log2 units) and sum
+    int grid;          // workgroups
+    int unit;          // keys that work is counted in, a multiple of 64 (16 rows)
+    int share_min;     // units of a workgroup, at least
+    float* part_o;     // [grid][2][16][D] unnormalised outputs of tiles that workgroups share
+    float* part_ml;    // [grid][2][16][2] maximum (log2 units) and sum
 };
 
 hipError_t launch_kv_append(const KvRowsArgs& a, int dtype, hipStream_t s);
@@ -52,10 +53,9 @@ hipError_t launch_kv_read(const KvRowsArgs& a, int dtype, hipStream_t s);
 
 // How an attention call is cut into workgroups; the same for the size query and the launch.
 struct KvAttnPlan {
-    unsigned slots;
-    int rows;    // rows of a tile
-    int Z, chunk;
-    int64_t ws;  // bytes of workspace
+    int grid, unit, share_min, nw;
+    int join_rows;  // rows of a tile that can be split, 0: no tile is
+    int64_t ws;     // bytes of workspace
 };
 KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int max_tokens, int max_context);
 hipError_t launch_kv_attention(KvAttnArgs a, const KvAttnPlan& p, int dtype, void* ws, hipStream_t s);
