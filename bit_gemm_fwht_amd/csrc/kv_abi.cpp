@@ -30,6 +30,7 @@ int check_batch(const fp4_kv_cache* c, const fp4_kv_batch* b, KvView* v) {
     if (!b->cu_tokens || !b->context || !b->table) return FP4_ERR_INVALID_ARG;
     if (b->seqs <= 0 || b->table_pages <= 0 || b->table_ld < b->table_pages || b->tokens < 0) return FP4_ERR_INVALID_ARG;
     if (b->max_tokens < 0 || b->max_context < 0) return FP4_ERR_INVALID_ARG;
+    if (c->pages > (int64_t(1) << 31) / c->kv_heads - 1) return FP4_ERR_UNSUPPORTED;  // blocks: 32 bits
     if (b->tokens > kMaxRows || b->seqs > kMaxRows / 4) return FP4_ERR_UNSUPPORTED;
     if (!aligned16(c->k_codes) || !aligned16(c->v_codes)) return FP4_ERR_ALIGNMENT;
     v->kc = reinterpret_cast<uint8_t*>(c->k_codes);

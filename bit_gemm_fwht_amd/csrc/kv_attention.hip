@@ -13,6 +13,7 @@
 // bytes of a channel of V as the cache stores it, and (page sizes being multiples of 16) lie in one
 // page, under one scale. Nothing is transposed and nothing moves between lanes but the statistics.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4_internal.h"
 #include "kv_device.h"
@@ -522,6 +523,392 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a) {
     if (a.lse && d == 0) a.lse[(int64_t)(t.tok0 + tok) * a.Hq + head] = lse_of(m, l);
 }
 
+// ---------------------------------------------------------------------------------------------
+// Many rows: tiles of 32 rows for each of eight waves. The workgroup brings 64 keys at a time into
+// LDS, once for all its rows: K as bf16 under its block scale, V as fp16 (both exact), converted on the
+// way, two buffers. A wave multiplies with 32x32x16 instructions; as above the accumulator of S^T is the
+// second operand of O^T's product, 16 consecutive keys in a lane.
+//
+// V's product runs in fp16, whose 11 bits hold the weights to 2^-12 where bf16 would hold them to 2^-9.
+// What fp16 lacks is range, so V's block exponent kv goes to the weight: with x = s + kv (log2 units)
+// a row's reference R is 11 below its largest x so far (to within kTileSlack) and
+//   p' = 2^(x - R) <= 2^15,   o = sum p' code,   l = sum p' 2^-kv,   out = o / l.
+// Exponents below kTileFloor are raised to it and V lowered instead (exact for another 2^-15), so that
+// blocks of zeros, whose exponent is -127, keep their weights in l. Steps with masks, where a row may
+// have few keys and one weight's rounding shows, and fp32 queries take each weight as two fp16.
+// ---------------------------------------------------------------------------------------------
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kTileKeys = 64;
+constexpr int kAheadK = 2, kAheadV = 3;  // products whose operands are read from LDS ahead of their turn
+constexpr float kTileSlack = 4.0f, kTileTop = 11.0f;
+constexpr int kTileFloor = -60;
+constexpr float kNoKeys = 1000.0f;  // exponent of 16 keys with no page: 2^-1000 = 0, and nothing overflows
+
+// 8 E4M3 codes times the power of two `scale` -> 8 fp16
+__device__ __forceinline__ u32x4 cvt8h(uint32_t a, uint32_t b, float scale) {
+    u32x4 r;
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, scale, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, scale, true));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, scale, false));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, scale, true));
+    return r;
+}
+// 8 weights as fp16, nearest even, and what is left of them
+__device__ __forceinline__ f16x8 weights8(const float* x) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){x[2 * i], x[2 * i + 1]}, f16x2));
+    return __builtin_bit_cast(f16x8, r);
+}
+__device__ __forceinline__ f16x8 rest8(const float* x, f16x8 h) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i] - (float)h[i];
+    return weights8(y);
+}
+
+// 16-byte pieces of a row of K (a key) and of V (a channel) in LDS, one more than its data so that rows
+// next to one another begin 4 banks apart: eight lanes of any access reach 32 banks.
+constexpr int tile_kp(int u) { return 8 * u + 1; }
+constexpr int kTileVp = kTileKeys / 8 + 1;
+
+// What one of 256 threads brings of each 64 keys of K (a key, and every fourth 16-byte piece of it) or
+// of V (16 keys of every 64th channel): from memory to registers, and a step later to LDS, converted.
+template <int U, bool FULL>
+struct TileStager {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const int32_t* row;  // the sequence's pages, from the one of key `tok` on
+    u32x4* dst;
+    uint32_t at, at_tok, at_u, page_bytes;
+    int tok;   // first key of the 64 that the thread brings
+    int need;  // its first channel
+    int last;  // index from `row` of the table's last page
+    bool is_v, there;
+    u32x4 raw[U];
+    uint32_t code;
+
+    __device__ __forceinline__ void init(const KvView& c, int D, int s, bool v, int id, u32x4* kt, u32x4* vt) {
+        const int r = id >> 2, q = id & 3;
+        is_v = v;
+        codes = v ? c.vc : c.kc;
+        scales = v ? c.vs : c.ks;
+        tok = v ? 16 * q : r;
+        need = v ? r : 16 * q;
+        row = c.table + (int64_t)s * c.table_ld;
+        last = c.W - 1;
+        const int srow = (r & 32) + 8 * ((r >> 2) & 3) + 4 * ((r >> 4) & 1) + (r & 3);  // S^T's row of key r
+        dst = v ? vt + r * kTileVp + 2 * q : kt + srow * tile_kp(U) + 2 * q;
+        page_bytes = (uint32_t)(c.P * D);
+        at_tok = v ? 1 : D;
+        at_u = v ? 64 * c.P : 64;
+        at = (v ? r * c.P : 16 * q) + (tok & (c.P - 1)) * at_tok;
+    }
+    // (kb is a multiple of 64 and tok below 64: the page index and the place in the page are each the
+    // sum of one of kb and one of tok)
+    __device__ __forceinline__ int entry(const KvView& c, int kb) const {
+        return row[min((kb >> c.pshift) + (tok >> c.pshift), last)];
+    }
+    __device__ __forceinline__ void load(const KvView& c, int h, int hi, int kb, int e, int D) {
+        there = kb + tok < hi && (uint32_t)e < (uint32_t)c.pages;
+        const uint32_t blk = (there ? (uint32_t)e : 0u) * (uint32_t)c.H + h;
+        code = scales[blk];
+        const uint8_t* p = codes + (uint64_t)blk * page_bytes + (at + (kb & (c.P - 1)) * at_tok);
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = *reinterpret_cast<const u32x4*>(p + (FULL || 64 * u + need < D ? (int)(u * at_u) : -(int)at));
+    }
+    __device__ __forceinline__ void stage(int D, const AttnTile& t, int kb, int buf, float* ve, int id) {
+        if (is_v) {
+            const int tv = kb + tok, kv = max((int)code - 127, kTileFloor);
+            const float scale = pow2f(max((int)code - 127 - kv, -126));
+            if (kb < t.lo || kb + kTileKeys > t.hi || __ballot(!there)) {  // what no row may attend is made zero
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int n1 = there ? min(max(t.hi - tv - 4 * j, 0), 4) : 0, n0 = min(max(t.lo - tv - 4 * j, 0), 4);
+                    uint32_t keep = n1 == 4 ? 0xFFFFFFFFu : (1u << (8 * n1)) - 1u;
+                    keep &= n0 == 4 ? 0u : 0xFFFFFFFFu << (8 * n0);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) raw[u][j] &= keep;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                u32x4* d = dst + buf * (64 * U * kTileVp) + 64 * u * kTileVp;
+                d[0] = cvt8h(raw[u][0], raw[u][1], scale);
+                d[1] = cvt8h(raw[u][2], raw[u][3], scale);
+            }
+            if (id < 4) ve[4 * buf + id] = there ? (float)kv : kNoKeys;
+        } else {
+            const float scale = e8m0_value(code);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                u32x4 w = raw[u];
+                if (!FULL && 64 * u + need >= D) w = (u32x4){0, 0, 0, 0};
+                u32x4* d = dst + buf * (kTileKeys * tile_kp(U)) + 8 * u;
+                d[0] = __builtin_bit_cast(u32x4, cvt8(w[0], w[1], scale));
+                d[1] = __builtin_bit_cast(u32x4, cvt8(w[2], w[3], scale));
+            }
+        }
+    }
+};
+
+// Eight waves, half of them bringing K and half V; four that bring both where registers ask for it.
+constexpr int tile_nw(int dt, int u) { return (dt == DT_BF16 ? u <= 2 : u == 1) ? 8 : 4; }
+
+template <int DT, int U, bool FULL>
+__global__ __launch_bounds__(64 * tile_nw(DT, U), tile_nw(DT, U) / 4) void k_kv_attn_tiles(KvAttnArgs a) {
+    constexpr int NS = DT == DT_BF16 ? 1 : 3, NW = tile_nw(DT, U), TR = 32 * NW;
+    constexpr int KP = tile_kp(U), VP = kTileVp;
+    const KvView& c = a.c;
+    const int D = FULL ? 64 * U : c.D;
+    // kv head fastest: workgroups go to the XCDs in turn, so the tiles of a head meet in one L2; the
+    // tiles at a sequence's end, with the most keys, first
+    const int h = blockIdx.x % c.H, slot = (int)a.slots - 1 - (int)(blockIdx.x / c.H);
+    int first;
+    const int s = find_sequence(c, slot, a.G, TR, 1, &first);
+    if (s < 0) return;
+    const AttnTile t = attn_tile<TR>(a, s, slot - first);
+    if (t.r0 >= t.r1) return;
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 31, hf = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    __shared__ u32x4 kt[2][kTileKeys * KP];
+    constexpr int NV = NW == 8 ? 3 : 2;  // buffers of V
+    __shared__ u32x4 vt[NV][64 * U * VP];
+    __shared__ float ve[NV][4];
+    constexpr int NB = NW == 8 ? 1 : 2;
+    TileStager<U, FULL> st[NB];
+    int entry[NB];
+    const int id = tid & 255;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) st[i].init(c, D, t.s, NW == 8 ? wave >= 4 : i == 1, id, &kt[0][0], &vt[0][0]);
+    const auto entries = [&](int kb) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) entry[i] = st[i].entry(c, kb);
+    };
+    const auto load = [&](int kb) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) st[i].load(c, h, t.hi, kb, entry[i], D);
+    };
+    const auto stage = [&](int buf, int vbuf, int kb) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) st[i].stage(D, t, kb, st[i].is_v ? vbuf : buf, &ve[0][0], id);
+    };
+
+    int kb = t.lo & ~(kTileKeys - 1);
+    entries(kb);
+    load(kb);
+    entries(kb + kTileKeys);
+
+    // the wave's 32 query rows, and the keys that some and that all of them may attend
+    const int r = t.r0 + 32 * wave + li;
+    const bool ok = r < t.r1;
+    const int tok = ok ? r / a.G : 0, head = h * a.G + (ok ? r - tok * a.G : 0), pos = t.p0 + tok;
+    const int row_hi = !ok ? 0 : a.causal ? min(t.keys, pos + 1) : t.keys;
+    const int row_lo = a.window ? pos - a.window + 1 : 0;
+    const int ra = t.r0 + 32 * wave, rb = min(ra + 32, t.r1) - 1;
+    const int pa = t.p0 + ra / a.G, pb = t.p0 + rb / a.G;
+    const int w_hi = ra > rb ? 0 : a.causal ? min(t.keys, pb + 1) : t.keys, w_lo = a.window ? pa - a.window + 1 : 0;
+    const int w_fhi = a.causal ? min(t.keys, pa + 1) : t.keys, w_flo = a.window ? pb - a.window + 1 : 0;
+    bf16x8 qf[NS][4 * U];
+    {
+        const int64_t q0 = (int64_t)(t.tok0 + tok) * a.ldq + (int64_t)head * a.ldq_head;
+#pragma unroll
+        for (int k = 0; k < 4 * U; ++k) {
+            const int d = 16 * k + 8 * hf;
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+            if (ok && (FULL || d < D)) {
+                if constexpr (DT == DT_BF16) {
+                    const u32x4 w = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.q) + q0 + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[2 * i] = bf16_lo(w[i]);
+                        x[2 * i + 1] = bf16_hi(w[i]);
+                    }
+                } else {
+                    const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(a.q) + q0 + d);
+                    const f32x4 w0 = p[0], w1 = p[1];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = w0[i], x[4 + i] = w1[i];
+                }
+            }
+            if (a.flip) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = -x[i];
+            }
+            bf16x8 f[NS];
+            split8<NS, true>(x, f);
+#pragma unroll
+            for (int n = 0; n < NS; ++n) qf[n][k] = f[n];
+        }
+    }
+    f32x16 o[2 * U];
+#pragma unroll
+    for (int i = 0; i < 2 * U; ++i) o[i] = (f32x16)(0.0f);
+    float R = kNegInf, l = 0.0f;
+    const float scale = __builtin_amdgcn_fmed3f(a.scale_log2, 1e-37f, 3.40282347e38f);
+
+    stage(0, 0, kb);
+    load(kb + kTileKeys);
+    entries(kb + 2 * kTileKeys);
+    __syncthreads();
+    int buf = 0, vbuf = 0;  // of this step
+    // Of eight waves the two halves (a wave of each on every SIMD) work half a step apart: while one
+    // multiplies (the weights of the step before with V, then K with q), the other is at its softmax, and
+    // the barriers between the halves of a step keep it so: waves of one SIMD in the same half compete
+    // for one unit and leave the other idle (166 us instead of 160 for the prompt below). In the half in
+    // which they multiply the first four waves write the next step's K to LDS and the last four its V: K
+    // takes the place of the K before this step's, which every wave is done with by then, and V, still
+    // wanted half a step longer, has three places. (Four waves write in the other half, all at once.)
+    const auto meet = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    f32x16 x[2];
+    f16x8 pf[4], pr[4];
+    const auto qk = [&](int buf) {
+        bf16x8 kf[4 * U][2];
+        const auto read_k = [&](int k) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) kf[k][j] = __builtin_bit_cast(bf16x8, kt[buf][(32 * j + li) * KP + 2 * k + hf]);
+        };
+#pragma unroll
+        for (int k = 0; k < kAheadK; ++k) read_k(k);
+#pragma unroll
+        for (int k = 0; k < 4 * U; ++k) {
+            if (k + kAheadK < 4 * U) read_k(k + kAheadK);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    x[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[k][j], qf[n][k], k + n ? x[j] : (f32x16)(0.0f), 0, 0, 0);
+        }
+    };
+    const auto pv = [&](int buf, const f16x8 (&w8)[4]) {
+        f16x8 vf[8 * U];
+        const auto read_v = [&](int n) {  // n: channels 32 (n % 2U) .., 8 keys n / 2U
+            const int i = n % (2 * U), w = n / (2 * U);
+            vf[n] = __builtin_bit_cast(f16x8, vt[buf][(32 * i + li) * VP + 4 * (w >> 1) + 2 * hf + (w & 1)]);
+        };
+#pragma unroll
+        for (int n = 0; n < kAheadV; ++n) read_v(n);
+#pragma unroll
+        for (int n = 0; n < 8 * U; ++n) {
+            const int i = n % (2 * U), w = n / (2 * U);
+            if (n + kAheadV < 8 * U) read_v(n + kAheadV);
+            __builtin_amdgcn_sched_barrier(0);
+            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[n], w8[w], o[i], 0, 0, 0);
+        }
+    };
+    const auto softmax = [&](int buf, int kb, const bool masked) {
+        const float kv[2] = {ve[buf][hf], ve[buf][2 + hf]};
+        if (masked) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = kb + 32 * j + 16 * hf + i;
+                    if (!(kv[j] != kNoKeys && key >= row_lo && key < row_hi)) x[j][i] = kNegInf;
+                }
+        }
+        float mx[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            mx[j] = x[j][0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) mx[j] = fmaxf(mx[j], x[j][i]);
+            mx[j] = __builtin_fmaf(mx[j], scale, kv[j] - kTileTop);
+        }
+        const float top = fmaxf(mx[0], mx[1]);
+        if (__ballot(top > R + kTileSlack)) {
+            const float rn = fmaxf(R, fmaxf(top, __shfl_xor(top, 32)));
+            const float f = __builtin_amdgcn_exp2f(R - (rn == kNegInf ? 0.0f : rn));
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < 2 * U; ++i) o[i] *= f;
+            R = rn;
+        }
+        const float rs = R == kNegInf ? 0.0f : R;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float off = kv[j] - rs;
+            float sum[4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j][i], scale, off));
+                sum[i & 3] = i < 4 ? x[j][i] : sum[i & 3] + x[j][i];
+            }
+            l = __builtin_fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), __builtin_amdgcn_exp2f(-kv[j]), l);
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            float p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = x[w >> 1][8 * (w & 1) + i];
+            pf[w] = weights8(p);
+        }
+        if (masked || DT == DT_F32) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                float p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] = x[w >> 1][8 * (w & 1) + i];
+                pr[w] = rest8(p, pf[w]);
+            }
+        }
+    };
+    int done = 0;  // what the step before left to multiply with V: 0 nothing, 1 weights, 2 and their rests
+    const auto multiply_v = [&](int buf) {
+        if (done) pv(buf, pf);
+        if (done == 2) pv(buf, pr);
+    };
+    if (NW == 8 && wave >= 4) meet();
+#pragma unroll 1
+    for (; kb < t.hi; kb += kTileKeys) {
+        const bool some = kb < w_hi && kb + kTileKeys > w_lo;
+        const int vlast = vbuf == 0 ? NV - 1 : vbuf - 1, vnext = vbuf == NV - 1 ? 0 : vbuf + 1;
+        multiply_v(vlast);
+        if (some) qk(buf);
+        if constexpr (NW == 8) stage(buf ^ 1, vnext, kb + kTileKeys);
+        meet();
+        done = 0;
+        if (some) {
+            const bool masked = kb < w_flo || kb + kTileKeys > w_fhi || __ballot(ve[vbuf][hf] == kNoKeys || ve[vbuf][2 + hf] == kNoKeys);
+            softmax(vbuf, kb, masked);
+            done = masked || DT == DT_F32 ? 2 : 1;
+        }
+        if constexpr (NW == 4) stage(buf ^ 1, vnext, kb + kTileKeys);
+        load(kb + 2 * kTileKeys);
+        entries(kb + 3 * kTileKeys);
+        meet();
+        buf ^= 1;
+        vbuf = vnext;
+    }
+    multiply_v(vbuf == 0 ? NV - 1 : vbuf - 1);
+    if (NW == 8 && wave < 4) meet();
+
+    l += __shfl_xor(l, 32);
+    if (!ok) return;
+    const float inv = safe_rcp(l);
+    const int64_t o0 = (int64_t)(t.tok0 + tok) * a.ldo + (int64_t)head * a.ldo_head + 4 * hf;
+#pragma unroll
+    for (int i = 0; i < 2 * U; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!FULL && 32 * i + 8 * e >= D) continue;
+            const f32x4 y = {o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+            store_out4<DT>(a.out, o0 + 32 * i + 8 * e, y * inv);
+        }
+    if (a.lse && hf == 0) a.lse[(int64_t)(t.tok0 + tok) * a.Hq + head] = lse_of(R, l);
+}
+
 static int cu_count() {
     int dev = 0, n = 0;
     if (hipGetDevice(&dev) != hipSuccess ||
@@ -530,9 +917,21 @@ static int cu_count() {
     return n;
 }
 
+constexpr int kTileRowsMin = 64;
+
 KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int max_tokens, int max_context) {
     KvAttnPlan p{};
     const int G = Hq / c.H;
+    // Many rows to a sequence (as far as the host knows: the average without a hint): tiles
+    const int64_t rows = max_tokens > 0 ? (int64_t)max_tokens * G : (int64_t)c.T * G / c.S;
+    if (rows >= kTileRowsMin) {
+        const int nw = tile_nw(dtype == DT_BF16 ? DT_BF16 : DT_F32, (c.D + 63) / 64);
+        const int64_t slots = (int64_t)c.T * G / (32 * nw) + c.S;
+        if (slots * c.H < (int64_t(1) << 31)) {
+            p.tile_slots = (int)slots;
+            return p;
+        }
+    }
     // tiles that have rows, and keys that one of them goes through, at most
     int64_t tiles = (int64_t)c.T * G / kRows + c.S;
     if (max_tokens > 0) tiles = std::min(tiles, c.S * (((int64_t)max_tokens * G + kRows - 1) / kRows));
@@ -574,6 +973,12 @@ static void launch_rows_nw(const KvAttnArgs& a, hipStream_t s) {
 
 template <int DT, int U>
 static void launch_rows(const KvAttnArgs& a, int nw, hipStream_t s) {
+    if (a.slots) {
+        const dim3 grid((unsigned)a.slots * a.c.H);
+        if (a.c.D == 64 * U) hipLaunchKernelGGL((k_kv_attn_tiles<DT, U, true>), grid, dim3(64 * tile_nw(DT, U)), 0, s, a);
+        else hipLaunchKernelGGL((k_kv_attn_tiles<DT, U, false>), grid, dim3(64 * tile_nw(DT, U)), 0, s, a);
+        return;
+    }
     if constexpr (rows_waves(DT, U) == 2) {
         if (nw == 8) return launch_rows_nw<DT, U, 8>(a, s);
     }
@@ -594,6 +999,7 @@ static hipError_t launch_dt(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_
 }
 
 hipError_t launch_kv_attention(KvAttnArgs a, const KvAttnPlan& p, int dtype, void* ws, hipStream_t s) {
+    a.slots = p.tile_slots;
     a.grid = p.grid;
     a.unit = p.unit;
     a.share_min = p.share_min;

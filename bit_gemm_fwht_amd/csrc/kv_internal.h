@@ -41,7 +41,8 @@ struct KvAttnArgs {
     float scale_log2;  // |scale| * log2(e)
     int flip;          // scale < 0: q is negated
     int causal, window;
-    int grid;          // workgroups
+    int slots;         // row tiles of the kernel for many rows (at least those that have rows)
+    int grid;          // workgroups of the kernel for few rows
     int unit;          // keys that work is counted in, a multiple of 64 (16 rows)
     int share_min;     // units of a workgroup, at least
     float* part_o;     // [grid][2][16][D] unnormalised outputs of tiles that workgroups share
@@ -53,6 +54,7 @@ hipError_t launch_kv_read(const KvRowsArgs& a, int dtype, hipStream_t s);
 
 // How an attention call is cut into workgroups; the same for the size query and the launch.
 struct KvAttnPlan {
+    int tile_slots;  // row tiles of the kernel for many rows, 0: the kernel for few
     int grid, unit, share_min, nw;
     int join_rows;  // rows of a tile that can be split, 0: no tile is
     int64_t ws;     // bytes of workspace
