@@ -655,12 +655,13 @@ struct TileStager {
     }
 };
 
-// Eight waves, half of them bringing K and half V; four that bring both where registers ask for it.
+// Eight waves, half of them bringing K and half V; four that bring both where registers ask for it, or
+// where tiles of 256 rows would leave CUs without one.
 constexpr int tile_nw(int dt, int u) { return (dt == DT_BF16 ? u <= 2 : u == 1) ? 8 : 4; }
 
-template <int DT, int U, bool FULL>
-__global__ __launch_bounds__(64 * tile_nw(DT, U), tile_nw(DT, U) / 4) void k_kv_attn_tiles(KvAttnArgs a) {
-    constexpr int NS = DT == DT_BF16 ? 1 : 3, NW = tile_nw(DT, U), TR = 32 * NW;
+template <int DT, int U, bool FULL, int NW>
+__global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(KvAttnArgs a) {
+    constexpr int NS = DT == DT_BF16 ? 1 : 3, TR = 32 * NW;
     constexpr int KP = tile_kp(U), VP = kTileVp;
     const KvView& c = a.c;
     const int D = FULL ? 64 * U : c.D;
@@ -917,33 +918,50 @@ static int cu_count() {
     return n;
 }
 
-constexpr int kTileRowsMin = 64;
-
 KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int max_tokens, int max_context) {
     KvAttnPlan p{};
-    const int G = Hq / c.H;
-    // Many rows to a sequence (as far as the host knows: the average without a hint): tiles
-    const int64_t rows = max_tokens > 0 ? (int64_t)max_tokens * G : (int64_t)c.T * G / c.S;
-    if (rows >= kTileRowsMin) {
-        const int nw = tile_nw(dtype == DT_BF16 ? DT_BF16 : DT_F32, (c.D + 63) / 64);
-        const int64_t slots = (int64_t)c.T * G / (32 * nw) + c.S;
-        if (slots * c.H < (int64_t(1) << 31)) {
-            p.tile_slots = (int)slots;
-            return p;
-        }
-    }
-    // tiles that have rows, and keys that one of them goes through, at most
-    int64_t tiles = (int64_t)c.T * G / kRows + c.S;
-    if (max_tokens > 0) tiles = std::min(tiles, c.S * (((int64_t)max_tokens * G + kRows - 1) / kRows));
-    tiles *= c.H;
+    const int G = Hq / c.H, U = (c.D + 63) / 64, cus = cu_count();
+    dtype = dtype == DT_BF16 ? DT_BF16 : DT_F32;
+    // keys that one tile goes through, at most
     const int64_t room = (int64_t)c.W << c.pshift;
     int64_t keys = room;
     if (max_context > 0) keys = std::min<int64_t>(keys, max_context);
     if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window + std::max(max_tokens, 1) + 64);
+    // tiles of r rows that have any, at most
+    const auto tiles_of = [&](int r) {
+        int64_t n = (int64_t)c.T * G / r + c.S;
+        if (max_tokens > 0) n = std::min(n, c.S * (((int64_t)max_tokens * G + r - 1) / r));
+        return n * c.H;
+    };
+    const int64_t tiles = tiles_of(kRows);
+
+    // Which kernel: by the time of their steps of 64 keys, as measured. In rows of 16 a wave's step takes
+    // 3 us (2.3 to 4.6), with 4 or 8 waves on a CU at a time whatever the number of tiles, and splitting and
+    // joining take about 15 us; in tiles a workgroup goes through all of its tile's keys: a step of four
+    // waves takes 1.65 us alone on a CU, 2.4 us with a second workgroup there or with eight waves, more
+    // where a lane holds more. (4096 tokens of 32 heads: 160 us in tiles, 390 us in rows; 512 rows of one
+    // head over 32000 keys: 799 us in tiles, 52 us in rows.) Tiles are of 128 rows unless there are more
+    // of them than two for a CU.
+    const bool wide = tile_nw(dtype, U) == 8;  // the variants of which two workgroups fit a CU
+    const int nw = wide && tiles_of(128) > 2 * cus ? 8 : 4;
+    const auto steps_of = [&](int r) {
+        const int64_t k = window > 0 ? std::min<int64_t>(keys, (int64_t)window + r / G + 64) : keys;
+        return (double)((k + 63) / 64);
+    };
+    const int64_t at_once = (int64_t)cus * (wide && nw == 4 ? 2 : 1), ntiles = tiles_of(32 * nw);
+    const double step_us = wide ? (nw == 4 && ntiles <= cus ? 1.65 : 2.4) : dtype == DT_BF16 ? 3.1 : U == 2 ? 3.0 : 7.6;
+    const double tiles_us = step_us * steps_of(32 * nw) * (double)((ntiles + at_once - 1) / at_once);
+    const double rows_us = 15.0 + 3.0 * steps_of(kRows) * (double)tiles / (4.0 * rows_waves(dtype, U) * cus);
+    const int64_t slots = (int64_t)c.T * G / (32 * nw) + c.S;
+    if ((int64_t)c.T * G >= 2 * kRows * (int64_t)c.S && tiles_us < rows_us && slots * c.H < (int64_t(1) << 31)) {
+        p.tile_slots = (int)slots;
+        p.nw = nw;
+        return p;
+    }
     // (the kernels count units in 32 bits, whatever the hints were)
     const int64_t most = ((int64_t)c.T * G / kRows + c.S) * c.H;
     const int64_t unit = 256;
-    const int waves = rows_waves(dtype == DT_BF16 ? DT_BF16 : DT_F32, (c.D + 63) / 64);
+    const int waves = rows_waves(dtype, U);
     if (keys <= 1024 || most * (room / unit + 1) >= (int64_t(1) << 31)) {
         // Short contexts: a workgroup for each tile, of eight waves where registers allow. 600 tokens of 8
         // kv heads: 11.7 us, against 13.5 + 4.2 us for shares and their join.
@@ -957,7 +975,7 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
         p.nw = 4;
         p.unit = (int)unit;
         p.share_min = 2;
-        p.grid = cu_count() * waves;
+        p.grid = cus * waves;
         p.join_rows = (int)std::min<int64_t>(max_tokens > 0 ? (int64_t)max_tokens * G : kRows, kRows);
         p.ws = (int64_t)p.grid * 2 * kRows * (c.D + 2) * 4;
     }
@@ -971,13 +989,20 @@ static void launch_rows_nw(const KvAttnArgs& a, hipStream_t s) {
     else hipLaunchKernelGGL((k_kv_attn_rows<DT, U, false, NW>), grid, dim3(64 * NW), 0, s, a);
 }
 
+template <int DT, int U, int NW>
+static void launch_tiles(const KvAttnArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)a.slots * a.c.H);
+    if (a.c.D == 64 * U) hipLaunchKernelGGL((k_kv_attn_tiles<DT, U, true, NW>), grid, dim3(64 * NW), 0, s, a);
+    else hipLaunchKernelGGL((k_kv_attn_tiles<DT, U, false, NW>), grid, dim3(64 * NW), 0, s, a);
+}
+
 template <int DT, int U>
-static void launch_rows(const KvAttnArgs& a, int nw, hipStream_t s) {
+static void launch_one(const KvAttnArgs& a, int nw, hipStream_t s) {
     if (a.slots) {
-        const dim3 grid((unsigned)a.slots * a.c.H);
-        if (a.c.D == 64 * U) hipLaunchKernelGGL((k_kv_attn_tiles<DT, U, true>), grid, dim3(64 * tile_nw(DT, U)), 0, s, a);
-        else hipLaunchKernelGGL((k_kv_attn_tiles<DT, U, false>), grid, dim3(64 * tile_nw(DT, U)), 0, s, a);
-        return;
+        if constexpr (tile_nw(DT, U) == 8) {
+            if (nw == 8) return launch_tiles<DT, U, 8>(a, s);
+        }
+        return launch_tiles<DT, U, 4>(a, s);
     }
     if constexpr (rows_waves(DT, U) == 2) {
         if (nw == 8) return launch_rows_nw<DT, U, 8>(a, s);
@@ -988,10 +1013,10 @@ static void launch_rows(const KvAttnArgs& a, int nw, hipStream_t s) {
 template <int DT>
 static hipError_t launch_dt(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t s) {
     switch ((a.c.D + 63) / 64) {
-        case 1: launch_rows<DT, 1>(a, p.nw, s); break;
-        case 2: launch_rows<DT, 2>(a, p.nw, s); break;
-        case 3: launch_rows<DT, 3>(a, p.nw, s); break;
-        default: launch_rows<DT, 4>(a, p.nw, s); break;
+        case 1: launch_one<DT, 1>(a, p.nw, s); break;
+        case 2: launch_one<DT, 2>(a, p.nw, s); break;
+        case 3: launch_one<DT, 3>(a, p.nw, s); break;
+        default: launch_one<DT, 4>(a, p.nw, s); break;
     }
     if (p.join_rows)
         hipLaunchKernelGGL((k_kv_attn_join<DT>), dim3((unsigned)p.join_rows, (unsigned)a.grid), dim3(256), 0, s, a);

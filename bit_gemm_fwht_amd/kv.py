@@ -24,6 +24,9 @@ import torch
 from . import fp4
 from .fp4 import DT_BF16, DT_F32, SCALE_E8M0_CEIL, SCALE_E8M0_FLOOR, Fp4Error, status_string
 
+# The current stream's handle by device index; the public way to it makes a Stream object first, which
+# takes a third of a small call's time on the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _CODES = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
 
 
@@ -149,6 +152,12 @@ def _use(cache: KVCache, batch: Batch, tokens: int) -> None:
     batch._c.tokens = tokens
 
 
+def _stream(dev: torch.device) -> int:
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
 def _check(status: int, what: str) -> None:
     if status != fp4.OK:
         raise Fp4Error(status, what)
@@ -163,7 +172,7 @@ def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, batch: Batch, scale
         raise ValueError("k and v must have one dtype and one number of tokens")
     _use(cache, batch, k.shape[0])
     st = lib().fp4_kv_append(cache._p, batch._p, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                             v.stride(1), code, scale_mode, torch.cuda.current_stream(dev).cuda_stream)
+                             v.stride(1), code, scale_mode, _stream(dev))
     _check(st, "fp4_kv_append")
 
 
@@ -181,7 +190,7 @@ def read(cache: KVCache, batch: Batch, tokens: int, dtype=torch.bfloat16, out=No
         raise ValueError(f"out must be two tensors of one dtype with {tokens} tokens")
     _use(cache, batch, tokens)
     st = lib().fp4_kv_read(cache._p, batch._p, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                           v.stride(1), code, torch.cuda.current_stream(dev).cuda_stream)
+                           v.stride(1), code, _stream(dev))
     _check(st, "fp4_kv_read")
     return k, v
 
@@ -209,7 +218,7 @@ def attention(q: torch.Tensor, cache: KVCache, batch: Batch, scale: float | None
     code = _rows(q, None, dim, dev, "q")
     tokens, heads = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif _rows(out, heads, dim, dev, "out") != code or out.shape[0] != tokens:
         raise ValueError("out must have q's shape and dtype")
     if lse is not None:
@@ -229,7 +238,7 @@ def attention(q: torch.Tensor, cache: KVCache, batch: Batch, scale: float | None
         else:
             fp4._ws_bytes(workspace, need, dev)
         ws = workspace.data_ptr()
-    st = L.fp4_kv_attention(cache._p, batch._p, pa, ws, need, torch.cuda.current_stream(dev).cuda_stream)
+    st = L.fp4_kv_attention(cache._p, batch._p, pa, ws, need, _stream(dev))
     _check(st, "fp4_kv_attention")
     return out
 
