@@ -1,5 +1,12 @@
 // The key / value cache: rows of K and V quantized into their pages as they are written, and read
-// back. One workgroup works for one block (page x kv head) of K or of V (grid z).
+// back. One wave works for one block (page x kv head) of K or of V; grid: blocks that the batch may
+// touch, kv heads by four, K and V.
+//
+// A lane takes 4 channels of 16 tokens at a time: the rows' side is then read and written in pieces of 4
+// values a token next to one another across the lanes, K's pages in 4 bytes a token likewise, and V's
+// pages, where a channel's tokens lie together, in 16 bytes a channel after a transposition in registers.
+// Nothing goes through LDS and no wave waits for another. Bound by memory: what it moves is what there
+// is to move.
 #include "fp4_internal.h"
 #include "kv_device.h"
 
@@ -38,22 +45,33 @@ __device__ __forceinline__ KvBlock kv_block(const KvView& c, int slot) {
     return b;
 }
 
+// 4 values of a row, as they are in memory
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
-    if constexpr (DT == DT_BF16) {
-        const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + at);
-        const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bf16_lo(q[i]);
-            v[2 * i + 1] = bf16_hi(q[i]);
+struct Row4 {
+    static constexpr int N = DT == DT_BF16 ? 2 : 4;
+    uint32_t w[N];
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
+        if constexpr (DT == DT_BF16) {
+            const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + at);
+            w[0] = v.x, w[1] = v.y;
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(p) + at);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
         }
-    } else {
-        const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
-        const float4 a = f[0], b = f[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
-}
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        if constexpr (DT == DT_BF16) {
+            v[0] = bf16_lo(w[0]), v[1] = bf16_hi(w[0]), v[2] = bf16_lo(w[1]), v[3] = bf16_hi(w[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+        }
+    }
+};
 
 // four E4M3 codes under a smaller scale: c * f, f = 2^(old - e) <= 1/2, nearest even
 __device__ __forceinline__ uint32_t requant4(uint32_t w, float f) {
@@ -62,114 +80,125 @@ __device__ __forceinline__ uint32_t requant4(uint32_t w, float f) {
     return cvt_fp8x2<true>(r, b[0] * f, b[1] * f, 1.0f);
 }
 
+// a 4 x 4 byte block transposed: byte j of word i becomes byte i of word j
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+    const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+    const uint32_t c = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+    w[0] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+    w[1] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    w[2] = __builtin_amdgcn_perm(d, c, 0x05040100u);
+    w[3] = __builtin_amdgcn_perm(d, c, 0x07060302u);
+}
+
 template <int DT>
 __global__ __launch_bounds__(kKvThreads) void k_kv_append(KvRowsArgs a) {
     const KvView& c = a.c;
-    const int h = blockIdx.y;
+    const int lane = threadIdx.x & 63;
+    const int h = blockIdx.y * (kKvThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (h >= c.H) return;
     const bool is_v = blockIdx.z != 0;
     const KvBlock b = kv_block(c, blockIdx.x);
     if (b.page < 0) return;
-    const int tid = threadIdx.x, D = c.D, P = c.P;
+    const int D = c.D, P = c.P, quads = D >> 2;
     const int64_t blk = (int64_t)b.page * c.H + h;
     uint8_t* codes = (is_v ? c.vc : c.kc) + blk * P * D;
     uint8_t* scales = (is_v ? c.vs : c.ks) + blk;
     const void* x = is_v ? a.v : a.k;
     const int64_t ld = is_v ? a.ldv : a.ldk;
     const int64_t x0 = (int64_t)b.row0 * ld + h * (is_v ? a.ldv_head : a.ldk_head);
-    const int per = D >> 3, chunks = (b.t1 - b.t0) * per;
-    __shared__ uint32_t smax[kKvThreads / 64];
-    __shared__ uint32_t tile[128 * 256 / 4];  // V: the new codes, [token][D], before their transposition
+    // tasks: a lane's 4 channels of 16 tokens; those that hold new tokens
+    const int g0 = b.t0 >> 4, tasks = (((b.t1 + 15) >> 4) - g0) * quads;
+    const bool held = tasks <= 64;  // one for a lane: read once
 
-    const uint32_t old_code = *scales;
+    const int old = (int)*scales - 127;
+    Row4<DT> r[16];
+    const auto load = [&](int i) {
+        const int g = g0 + i / quads, d = (i % quads) * 4;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            const int at = 16 * g + t;
+            if (at >= b.t0 && at < b.t1) r[t].load(x, x0 + (int64_t)(at - b.t0) * ld + d);
+            else r[t].zero();
+        }
+    };
     // amax of the new tokens (as integers: |x| orders like its bits)
     uint32_t m = 0;
-    for (int i = tid; i < chunks; i += kKvThreads) {
-        const int t = i / per, d = (i - t * per) * 8;
-        float v[8];
-        load8<DT>(x, x0 + t * ld + d, v);
+    for (int i = lane; i < tasks; i += 64) {
+        load(i);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        for (int t = 0; t < 16; ++t) {
+            float v[4];
+            r[t].get(v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        }
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
-    if ((tid & 63) == 0) smax[tid >> 6] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kKvThreads / 64; ++i) m = max(m, smax[i]);
     int e = e8m0_exp<8, 0x600000u>(__uint_as_float(m), a.ceil_rule != 0);
-    if (b.begun) e = max(e, (int)old_code - 127);
-    if (tid == 0) *scales = (uint8_t)(e + 127);
-
-    if (b.begun && e + 127 > (int)old_code) {  // the older tokens under the block's new scale
-        const int diff = (int)old_code - 127 - e;
-        const float f = __builtin_amdgcn_ldexpf(1.0f, diff);
-        if (is_v) {
-            const int groups = (b.t0 + 15) >> 4;
-            for (int i = tid; i < D * groups; i += kKvThreads) {
-                const int d = i / groups, g = i - d * groups;
-                uint4* p = reinterpret_cast<uint4*>(codes + d * P + 16 * g);
-                const uint4 v = *p;
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {  // bytes of the places before t0 only
-                    const int n = min(max(b.t0 - 16 * g - 4 * j, 0), 4);
-                    const uint32_t old = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
-                    w[j] = (requant4(w[j], f) & old) | (w[j] & ~old);
-                }
-                *p = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        } else {
-            for (int i = tid; i < b.t0 * (D >> 4); i += kKvThreads) {
-                uint4* p = reinterpret_cast<uint4*>(codes) + i;
-                uint4 w = *p;
-                w = make_uint4(requant4(w.x, f), requant4(w.y, f), requant4(w.z, f), requant4(w.w, f));
-                *p = w;
-            }
-        }
-        __syncthreads();
-    }
+    if (b.begun) e = max(e, old);
+    const bool grown = b.begun && e > old;  // the older tokens get the block's new scale
+    const float f = __builtin_amdgcn_ldexpf(1.0f, grown ? old - e : 0);
+    if (lane == 0) *scales = (uint8_t)(e + 127);
 
     // the new tokens: x * 2^-e by the scaled convert, which divides by 2^e exactly; 2^-127 is not a
     // normal fp32, so that exponent is reached by doubling x
     const float dbl = e == -127 ? 2.0f : 1.0f;
     const float sc = pow2f(max(e, -126));
     const float lim = fminf(448.0f * sc, 3.40282347e38f);
-    uint8_t* const tb = reinterpret_cast<uint8_t*>(tile);
-    for (int i = tid; i < chunks; i += kKvThreads) {
-        const int t = i / per, d = (i - t * per) * 8;
-        float v[8];
-        load8<DT>(x, x0 + t * ld + d, v);
-        uint32_t r[2];
+    for (int i = lane; i < tasks; i += 64) {
+        if (!held) load(i);
+        const int g = g0 + i / quads, d = (i % quads) * 4;
+        uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __builtin_amdgcn_fmed3f(v[j] * dbl, -lim, lim);
+        for (int t = 0; t < 16; ++t) {
+            float v[4];
+            r[t].get(v);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            r[j] = cvt_fp8x2<false>(0u, v[4 * j], v[4 * j + 1], sc);
-            r[j] = cvt_fp8x2<true>(r[j], v[4 * j + 2], v[4 * j + 3], sc);
+            for (int j = 0; j < 4; ++j) v[j] = __builtin_amdgcn_fmed3f(v[j] * dbl, -lim, lim);
+            w[t] = cvt_fp8x2<false>(0u, v[0], v[1], sc);
+            w[t] = cvt_fp8x2<true>(w[t], v[2], v[3], sc);
         }
-        uint8_t* dst = is_v ? tb + t * D + d : codes + (b.t0 + t) * D + d;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(r[0], r[1]);
-    }
-    if (!is_v) return;
-    __syncthreads();
-    // V goes to the page channel by channel: 16 tokens at once where all 16 are new, else bytes
-    const int g0 = b.t0 >> 4, groups = ((b.t1 + 15) >> 4) - g0;
-    for (int i = tid; i < D * groups; i += kKvThreads) {
-        const int g = i / D, d = i - g * D;
-        const int lo = (g0 + g) * 16;
-        uint8_t* dst = codes + d * P + lo;
-        if (lo >= b.t0 && lo + 16 <= b.t1) {
-            uint32_t w[4];
+        const int lo = b.t0 - 16 * g, hi = b.t1 - 16 * g;  // new places of these 16: [lo, hi)
+        if (!is_v) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[j] = 0;
+            for (int t = 0; t < 16; ++t)
+                if (t >= lo && t < hi) *reinterpret_cast<uint32_t*>(codes + (16 * g + t) * D + d) = w[t];
+            continue;
+        }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[j] |= (uint32_t)tb[(lo - b.t0 + 4 * j + k) * D + d] << (8 * k);
+        for (int q = 0; q < 4; ++q) {
+            uint32_t s4[4] = {w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
+            transpose4(s4);  // s4[j]: channel d + j of tokens 4 q .. 4 q + 3
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[4 * q + j] = s4[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4* p = reinterpret_cast<uint4*>(codes + (d + j) * P + 16 * g);
+            uint32_t n[4] = {w[j], w[4 + j], w[8 + j], w[12 + j]};
+            if (lo > 0 || hi < 16) {  // places before lo: older tokens; from hi on: left as they are
+                const uint4 v = *p;
+                const uint32_t was[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int nl = min(max(lo - 4 * q, 0), 4), nh = min(max(hi - 4 * q, 0), 4);
+                    const uint32_t before = nl == 4 ? 0xFFFFFFFFu : (1u << (8 * nl)) - 1u;
+                    const uint32_t upto = nh == 4 ? 0xFFFFFFFFu : (1u << (8 * nh)) - 1u;
+                    const uint32_t older = grown ? requant4(was[q], f) : was[q];
+                    n[q] = (older & before) | (n[q] & upto & ~before) | (was[q] & ~(upto | before));
+                }
             }
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            for (int t = max(lo, b.t0); t < min(lo + 16, b.t1); ++t) dst[t - lo] = tb[(t - b.t0) * D + d];
+            *p = make_uint4(n[0], n[1], n[2], n[3]);
         }
+    }
+    if (!grown) return;
+    // older tokens elsewhere in the block: K's rows, V's groups of 16 without a new token
+    const int pieces = is_v ? D * g0 : b.t0 * (D >> 4);
+    for (int i = lane; i < pieces; i += 64) {
+        uint4* p = reinterpret_cast<uint4*>(is_v ? codes + (i / g0) * P + 16 * (i % g0) : codes + 16 * i);
+        const uint4 w = *p;
+        *p = make_uint4(requant4(w.x, f), requant4(w.y, f), requant4(w.z, f), requant4(w.w, f));
     }
 }
 
@@ -195,48 +224,53 @@ __device__ __forceinline__ void store4(void* p, int64_t at, const float (&y)[4])
 template <int DT>
 __global__ __launch_bounds__(kKvThreads) void k_kv_read(KvRowsArgs a) {
     const KvView& c = a.c;
-    const int h = blockIdx.y;
+    const int lane = threadIdx.x & 63;
+    const int h = blockIdx.y * (kKvThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (h >= c.H) return;
     const bool is_v = blockIdx.z != 0;
     const KvBlock b = kv_block(c, blockIdx.x);
     if (b.page < 0) return;
-    const int tid = threadIdx.x, D = c.D, P = c.P;
+    const int D = c.D, P = c.P, quads = D >> 2;
     const int64_t blk = (int64_t)b.page * c.H + h;
     const uint8_t* codes = (is_v ? c.vc : c.kc) + blk * P * D;
     const int e = (int)(is_v ? c.vs : c.ks)[blk] - 127;
     void* y = const_cast<void*>(is_v ? a.v : a.k);
     const int64_t ld = is_v ? a.ldv : a.ldk;
     const int64_t y0 = (int64_t)b.row0 * ld + h * (is_v ? a.ldv_head : a.ldk_head);
-    const int per = D >> 2, n = b.t1 - b.t0;
-    __shared__ uint32_t tile[256 * (128 / 4 + 1)];  // V: the page, channels 4 bytes apart beyond P
-    const int pitch = P + 4;
-    const uint8_t* tb = reinterpret_cast<const uint8_t*>(tile);
-    if (is_v) {
-        const int groups = P >> 4;
-        for (int i = tid; i < D * groups; i += kKvThreads) {
-            const int d = i / groups, g = i - d * groups;
-            const uint4 w = *reinterpret_cast<const uint4*>(codes + d * P + 16 * g);
-            uint32_t* dst = tile + (d * pitch + 16 * g) / 4;
-            dst[0] = w.x, dst[1] = w.y, dst[2] = w.z, dst[3] = w.w;
-        }
-        __syncthreads();
-    }
-    for (int i = tid; i < n * per; i += kKvThreads) {
-        const int t = i / per, d = (i - t * per) * 4;
-        uint32_t w;
+    const int g0 = b.t0 >> 4, tasks = (((b.t1 + 15) >> 4) - g0) * quads;
+    for (int i = lane; i < tasks; i += 64) {
+        const int g = g0 + i / quads, d = (i % quads) * 4;
+        uint32_t w[16];  // 4 channels of each of the 16 tokens
         if (is_v) {
-            const uint8_t* p = tb + d * pitch + b.t0 + t;
-            w = (uint32_t)p[0] | ((uint32_t)p[pitch] << 8) | ((uint32_t)p[2 * pitch] << 16) | ((uint32_t)p[3 * pitch] << 24);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 v = *reinterpret_cast<const uint4*>(codes + (d + j) * P + 16 * g);
+                w[j] = v.x, w[4 + j] = v.y, w[8 + j] = v.z, w[12 + j] = v.w;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t s4[4] = {w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
+                transpose4(s4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[4 * q + j] = s4[j];
+            }
         } else {
-            w = *reinterpret_cast<const uint32_t*>(codes + (b.t0 + t) * D + d);
+#pragma unroll
+            for (int t = 0; t < 16; ++t) w[t] = *reinterpret_cast<const uint32_t*>(codes + (16 * g + t) * D + d);
         }
-        float v[4];
-        decode4(w, e, v);
-        store4<DT>(y, y0 + t * ld + d, v);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            const int at = 16 * g + t;
+            if (at < b.t0 || at >= b.t1) continue;
+            float v[4];
+            decode4(w[t], e, v);
+            store4<DT>(y, y0 + (int64_t)(at - b.t0) * ld + d, v);
+        }
     }
 }
 
 static dim3 kv_grid(const KvView& c) {
-    return dim3((unsigned)(c.T / c.P + 2 * c.S), (unsigned)c.H, 2);
+    return dim3((unsigned)(c.T / c.P + 2 * c.S), (unsigned)((c.H + kKvThreads / 64 - 1) / (kKvThreads / 64)), 2);
 }
 
 hipError_t launch_kv_append(const KvRowsArgs& a, int dtype, hipStream_t s) {
