@@ -524,51 +524,16 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Many rows: tiles of 32 rows for each of eight waves. The workgroup brings 64 keys at a time into
-// LDS, once for all its rows: K as bf16 under its block scale, V as fp16 (both exact), converted on the
-// way, two buffers. A wave multiplies with 32x32x16 instructions; as above the accumulator of S^T is the
-// second operand of O^T's product, 16 consecutive keys in a lane.
-//
-// V's product runs in fp16, whose 11 bits hold the weights to 2^-12 where bf16 would hold them to 2^-9.
-// What fp16 lacks is range, so V's block exponent kv goes to the weight: with x = s + kv (log2 units)
-// a row's reference R is 11 below its largest x so far (to within kTileSlack) and
-//   p' = 2^(x - R) <= 2^15,   o = sum p' code,   l = sum p' 2^-kv,   out = o / l.
-// Exponents below kTileFloor are raised to it and V lowered instead (exact for another 2^-15), so that
-// blocks of zeros, whose exponent is -127, keep their weights in l. Steps with masks, where a row may
-// have few keys and one weight's rounding shows, and fp32 queries take each weight as two fp16.
+// Many rows: tiles of 32 rows for each of eight (or four) waves. The workgroup brings 64 keys at a time
+// into LDS, once for all its rows, as bf16 under their blocks' scales (exact), converted on the way. A
+// wave multiplies with 32x32x16 instructions; as above the accumulator of S^T is, once exponentials are
+// taken, the second operand of O^T's product: 16 consecutive keys in a lane. Weights enter as sums of two
+// bf16 (fp32 queries: three), cut and rounded next to the products, where the vector unit has time.
+// (Weights as one fp16 each take 160 us instead of 206 for a prompt of 4096 tokens and 32 heads, but lose channels to which
+// only keys of small weight contribute: fp16 ends 2^-24 below 1.)
 // ---------------------------------------------------------------------------------------------
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-
 constexpr int kTileKeys = 64;
 constexpr int kAheadK = 2, kAheadV = 3;  // products whose operands are read from LDS ahead of their turn
-constexpr float kTileSlack = 4.0f, kTileTop = 11.0f;
-constexpr int kTileFloor = -60;
-constexpr float kNoKeys = 1000.0f;  // exponent of 16 keys with no page: 2^-1000 = 0, and nothing overflows
-
-// 8 E4M3 codes times the power of two `scale` -> 8 fp16
-__device__ __forceinline__ u32x4 cvt8h(uint32_t a, uint32_t b, float scale) {
-    u32x4 r;
-    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, scale, false));
-    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, scale, true));
-    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, scale, false));
-    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, scale, true));
-    return r;
-}
-// 8 weights as fp16, nearest even, and what is left of them
-__device__ __forceinline__ f16x8 weights8(const float* x) {
-    u32x4 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        r[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f){x[2 * i], x[2 * i + 1]}, f16x2));
-    return __builtin_bit_cast(f16x8, r);
-}
-__device__ __forceinline__ f16x8 rest8(const float* x, f16x8 h) {
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i] - (float)h[i];
-    return weights8(y);
-}
 
 // 16-byte pieces of a row of K (a key) and of V (a channel) in LDS, one more than its data so that rows
 // next to one another begin 4 banks apart: eight lanes of any access reach 32 banks.
@@ -620,10 +585,10 @@ struct TileStager {
 #pragma unroll
         for (int u = 0; u < U; ++u) raw[u] = *reinterpret_cast<const u32x4*>(p + (FULL || 64 * u + need < D ? (int)(u * at_u) : -(int)at));
     }
-    __device__ __forceinline__ void stage(int D, const AttnTile& t, int kb, int buf, float* ve, int id) {
+    __device__ __forceinline__ void stage(int D, const AttnTile& t, int kb, int buf, int* some, int id) {
+        const float scale = e8m0_value(code);
         if (is_v) {
-            const int tv = kb + tok, kv = max((int)code - 127, kTileFloor);
-            const float scale = pow2f(max((int)code - 127 - kv, -126));
+            const int tv = kb + tok;
             if (kb < t.lo || kb + kTileKeys > t.hi || __ballot(!there)) {  // what no row may attend is made zero
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -637,12 +602,11 @@ struct TileStager {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 u32x4* d = dst + buf * (64 * U * kTileVp) + 64 * u * kTileVp;
-                d[0] = cvt8h(raw[u][0], raw[u][1], scale);
-                d[1] = cvt8h(raw[u][2], raw[u][3], scale);
+                d[0] = __builtin_bit_cast(u32x4, cvt8(raw[u][0], raw[u][1], scale));
+                d[1] = __builtin_bit_cast(u32x4, cvt8(raw[u][2], raw[u][3], scale));
             }
-            if (id < 4) ve[4 * buf + id] = there ? (float)kv : kNoKeys;
+            if (id < 4) some[4 * buf + id] = there;
         } else {
-            const float scale = e8m0_value(code);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 u32x4 w = raw[u];
@@ -661,7 +625,7 @@ constexpr int tile_nw(int dt, int u) { return (dt == DT_BF16 ? u <= 2 : u == 1) 
 
 template <int DT, int U, bool FULL, int NW>
 __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(KvAttnArgs a) {
-    constexpr int NS = DT == DT_BF16 ? 1 : 3, TR = 32 * NW;
+    constexpr int NS = DT == DT_BF16 ? 1 : 3, NP = DT == DT_BF16 ? 2 : 3, TR = 32 * NW;
     constexpr int KP = tile_kp(U), VP = kTileVp;
     const KvView& c = a.c;
     const int D = FULL ? 64 * U : c.D;
@@ -679,7 +643,7 @@ __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(K
     __shared__ u32x4 kt[2][kTileKeys * KP];
     constexpr int NV = NW == 8 ? 3 : 2;  // buffers of V
     __shared__ u32x4 vt[NV][64 * U * VP];
-    __shared__ float ve[NV][4];
+    __shared__ int there[NV][4];  // whether each 16 keys have a page
     constexpr int NB = NW == 8 ? 1 : 2;
     TileStager<U, FULL> st[NB];
     int entry[NB];
@@ -696,7 +660,7 @@ __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(K
     };
     const auto stage = [&](int buf, int vbuf, int kb) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i) st[i].stage(D, t, kb, st[i].is_v ? vbuf : buf, &ve[0][0], id);
+        for (int i = 0; i < NB; ++i) st[i].stage(D, t, kb, st[i].is_v ? vbuf : buf, &there[0][0], id);
     };
 
     int kb = t.lo & ~(kTileKeys - 1);
@@ -751,7 +715,7 @@ __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(K
     f32x16 o[2 * U];
 #pragma unroll
     for (int i = 0; i < 2 * U; ++i) o[i] = (f32x16)(0.0f);
-    float R = kNegInf, l = 0.0f;
+    float m = kNegInf, l = 0.0f;
     const float scale = __builtin_amdgcn_fmed3f(a.scale_log2, 1e-37f, 3.40282347e38f);
 
     stage(0, 0, kb);
@@ -771,8 +735,7 @@ __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(K
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
     };
-    f32x16 x[2];
-    f16x8 pf[4], pr[4];
+    f32x16 x[2];  // q.k, then weights
     const auto qk = [&](int buf) {
         bf16x8 kf[4 * U][2];
         const auto read_k = [&](int k) {
@@ -792,98 +755,79 @@ __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(K
                     x[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[k][j], qf[n][k], k + n ? x[j] : (f32x16)(0.0f), 0, 0, 0);
         }
     };
-    const auto pv = [&](int buf, const f16x8 (&w8)[4]) {
-        f16x8 vf[8 * U];
+    const auto pv = [&](int buf) {
+        bf16x8 vf[8 * U];
         const auto read_v = [&](int n) {  // n: channels 32 (n % 2U) .., 8 keys n / 2U
             const int i = n % (2 * U), w = n / (2 * U);
-            vf[n] = __builtin_bit_cast(f16x8, vt[buf][(32 * i + li) * VP + 4 * (w >> 1) + 2 * hf + (w & 1)]);
+            vf[n] = __builtin_bit_cast(bf16x8, vt[buf][(32 * i + li) * VP + 4 * (w >> 1) + 2 * hf + (w & 1)]);
         };
 #pragma unroll
         for (int n = 0; n < kAheadV; ++n) read_v(n);
-#pragma unroll
-        for (int n = 0; n < 8 * U; ++n) {
-            const int i = n % (2 * U), w = n / (2 * U);
-            if (n + kAheadV < 8 * U) read_v(n + kAheadV);
-            __builtin_amdgcn_sched_barrier(0);
-            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[n], w8[w], o[i], 0, 0, 0);
-        }
-    };
-    const auto softmax = [&](int buf, int kb, const bool masked) {
-        const float kv[2] = {ve[buf][hf], ve[buf][2 + hf]};
-        if (masked) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = kb + 32 * j + 16 * hf + i;
-                    if (!(kv[j] != kNoKeys && key >= row_lo && key < row_hi)) x[j][i] = kNegInf;
-                }
-        }
-        float mx[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            mx[j] = x[j][0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) mx[j] = fmaxf(mx[j], x[j][i]);
-            mx[j] = __builtin_fmaf(mx[j], scale, kv[j] - kTileTop);
-        }
-        const float top = fmaxf(mx[0], mx[1]);
-        if (__ballot(top > R + kTileSlack)) {
-            const float rn = fmaxf(R, fmaxf(top, __shfl_xor(top, 32)));
-            const float f = __builtin_amdgcn_exp2f(R - (rn == kNegInf ? 0.0f : rn));
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < 2 * U; ++i) o[i] *= f;
-            R = rn;
-        }
-        const float rs = R == kNegInf ? 0.0f : R;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float off = kv[j] - rs;
-            float sum[4];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j][i], scale, off));
-                sum[i & 3] = i < 4 ? x[j][i] : sum[i & 3] + x[j][i];
-            }
-            l = __builtin_fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), __builtin_amdgcn_exp2f(-kv[j]), l);
-        }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             float p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) p[i] = x[w >> 1][8 * (w & 1) + i];
-            pf[w] = weights8(p);
-        }
-        if (masked || DT == DT_F32) {
+            bf16x8 pf[NP];
+            split8<NP, false>(p, pf);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                float p[8];
+            for (int i = 0; i < 2 * U; ++i) {
+                const int n = 2 * U * w + i;
+                if (n + kAheadV < 8 * U) read_v(n + kAheadV);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i] = x[w >> 1][8 * (w & 1) + i];
-                pr[w] = rest8(p, pf[w]);
+                for (int q = 0; q < NP; ++q) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[n], pf[q], o[i], 0, 0, 0);
             }
         }
     };
-    int done = 0;  // what the step before left to multiply with V: 0 nothing, 1 weights, 2 and their rests
-    const auto multiply_v = [&](int buf) {
-        if (done) pv(buf, pf);
-        if (done == 2) pv(buf, pr);
+    const auto softmax = [&](int buf, int kb, const bool masked) {
+        if (masked) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool page = there[buf][2 * j + hf] != 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = kb + 32 * j + 16 * hf + i;
+                    if (!(page && key >= row_lo && key < row_hi)) x[j][i] = kNegInf;
+                }
+            }
+        }
+        float mx = x[0][0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) mx = fmaxf(mx, x[i >> 4][i & 15]);
+        mx *= scale;
+        if (__ballot(mx > m + kSlack)) {
+            const float mn = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32)));
+            const float f = __builtin_amdgcn_exp2f(m - (mn == kNegInf ? 0.0f : mn));
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < 2 * U; ++i) o[i] *= f;
+            m = mn;
+        }
+        const float ms = m == kNegInf ? 0.0f : m;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i >> 4][i & 15], scale, -ms));
+            x[i >> 4][i & 15] = p;
+            sum[i & 3] += p;
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
+    bool weights = false;  // whether the step before left any to multiply with V
     if (NW == 8 && wave >= 4) meet();
 #pragma unroll 1
     for (; kb < t.hi; kb += kTileKeys) {
         const bool some = kb < w_hi && kb + kTileKeys > w_lo;
         const int vlast = vbuf == 0 ? NV - 1 : vbuf - 1, vnext = vbuf == NV - 1 ? 0 : vbuf + 1;
-        multiply_v(vlast);
+        if (weights) pv(vlast);
         if (some) qk(buf);
         if constexpr (NW == 8) stage(buf ^ 1, vnext, kb + kTileKeys);
         meet();
-        done = 0;
+        weights = some;
         if (some) {
-            const bool masked = kb < w_flo || kb + kTileKeys > w_fhi || __ballot(ve[vbuf][hf] == kNoKeys || ve[vbuf][2 + hf] == kNoKeys);
-            softmax(vbuf, kb, masked);
-            done = masked || DT == DT_F32 ? 2 : 1;
+            const int* at = there[vbuf];
+            softmax(vbuf, kb, kb < w_flo || kb + kTileKeys > w_fhi || !(at[0] && at[1] && at[2] && at[3]));
         }
         if constexpr (NW == 4) stage(buf ^ 1, vnext, kb + kTileKeys);
         load(kb + 2 * kTileKeys);
@@ -892,7 +836,7 @@ __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(K
         buf ^= 1;
         vbuf = vnext;
     }
-    multiply_v(vbuf == 0 ? NV - 1 : vbuf - 1);
+    if (weights) pv(vbuf == 0 ? NV - 1 : vbuf - 1);
     if (NW == 8 && wave < 4) meet();
 
     l += __shfl_xor(l, 32);
@@ -907,7 +851,7 @@ __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(K
             const f32x4 y = {o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
             store_out4<DT>(a.out, o0 + 32 * i + 8 * e, y * inv);
         }
-    if (a.lse && hf == 0) a.lse[(int64_t)(t.tok0 + tok) * a.Hq + head] = lse_of(R, l);
+    if (a.lse && hf == 0) a.lse[(int64_t)(t.tok0 + tok) * a.Hq + head] = lse_of(m, l);
 }
 
 static int cu_count() {
@@ -962,9 +906,10 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
     const int64_t most = ((int64_t)c.T * G / kRows + c.S) * c.H;
     const int64_t unit = 256;
     const int waves = rows_waves(dtype, U);
-    if (keys <= 1024 || most * (room / unit + 1) >= (int64_t(1) << 31)) {
-        // Short contexts: a workgroup for each tile, of eight waves where registers allow. 600 tokens of 8
-        // kv heads: 11.7 us, against 13.5 + 4.2 us for shares and their join.
+    if (keys <= 2048 || most * (room / unit + 1) >= (int64_t(1) << 31)) {
+        // Short contexts: a workgroup for each tile, of eight waves where registers allow, and one launch
+        // (600 tokens of 8 kv heads: 11.7 us, in shares 13.5 + 4.2 us for the join; 64 sequences of up to
+        // 2000 tokens: 41 us against 50, all of 2000: 60 us against 57).
         p.nw = 4 * waves;
         p.unit = 1 << 30;
         p.share_min = 1;

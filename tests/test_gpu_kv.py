@@ -437,3 +437,65 @@ def test_binding_refuses_wrong_tensors():
         kv.attention(torch.randn(2, 4, 64, device=DEV), c, s.batch, lse=torch.zeros(2, 4))
     with pytest.raises(ValueError):
         kv.attention(torch.randn(2, 4, 64, device=DEV), c, s.batch, out=torch.zeros(2, 4, 64, device=DEV).bfloat16())
+
+
+# -------------------------------------------------------- prompts: the kernel for many rows, both tile sizes
+PROMPTS = {
+    "whole": ([(700, 700)], 2, 3),
+    "uneven": ([(300, 300), (1, 900), (0, 7), (129, 640), (64, 64)], 2, 4),
+    "behind a context": ([(256, 1500), (33, 2000)], 4, 2),
+    "many sequences": ([(40, 40 + i) for i in range(66)], 8, 2),  # tiles of 256 rows are too many for 128
+    "no tokens before": ([(200, 150), (90, 90)], 2, 4),            # rows before the first token
+}
+
+
+@pytest.mark.parametrize("prompt", PROMPTS)
+@pytest.mark.parametrize("dim,page,dtype", [(128, 32, "bf16"), (64, 16, "bf16"), (48, 128, "bf16"), (112, 64, "bf16"),
+                                            (256, 32, "bf16"), (64, 64, "f32"), (128, 16, "f32")])
+def test_attention_of_prompts(prompt, dim, page, dtype):
+    lens, heads, group = PROMPTS[prompt]
+    s = Setup(lens, heads, dim, page, seed=20, fill=0x7F)
+    check_attention(s, heads * group, dtype)
+
+
+@pytest.mark.parametrize("causal,window,scale", [(False, 0, None), (True, 100, None), (False, 77, None), (True, 1, None),
+                                                 (True, 0, -0.2), (True, 0, 0.0), (True, 300, 3.0)])
+def test_attention_of_prompts_masks_and_scales(causal, window, scale):
+    lens, heads, group = PROMPTS["uneven"]
+    s = Setup(lens, heads, 128, 32, seed=21, fill=0xFF)
+    check_attention(s, heads * group, "bf16", causal=causal, window=window, scale=scale)
+
+
+@pytest.mark.parametrize("low,high", [(-60, 60), (-20, 20), (-90, -90), (40, 40)])
+def test_attention_of_prompts_with_blocks_of_uneven_size(low, high):
+    """V's block exponents far apart, and all of them far from one; blocks of zeros among them (exponent
+    -127, whose keys have their weights all the same)."""
+    s = Setup([(500, 500)], 2, 64, 32, seed=22)
+    r = s.ref
+    r.vs[:] = np.where(np.arange(r.pages)[:, None] % 2, 127 + high, 127 + low)
+    r.v[s.table[0, 5]] = 0
+    r.vs[s.table[0, 5]] = 0
+    s.cache.v_codes.copy_(torch.from_numpy(r.v))
+    s.cache.v_scales.copy_(torch.from_numpy(r.vs))
+    if low == -90:  # fp16 keeps what is above 2^-84 here: the absolute bound of the layout's description
+        o = kv.attention(s.draw(4, "f32"), s.cache, s.batch)
+        assert torch.isfinite(o).all() and o.abs().max() <= 448 * 2.0 ** -90
+    else:
+        check_attention(s, 4, "bf16")
+
+
+def test_attention_of_prompts_with_pages_missing():
+    s = Setup([(300, 600)], 2, 64, 16, seed=23)
+    s.table[0, [7, 20, 30]] = [-1, s.ref.pages, 1 << 30]
+    s.batch.table.copy_(torch.from_numpy(s.table))
+    check_attention(s, 4, "bf16")
+
+
+def test_attention_does_not_depend_on_what_else_is_in_the_batch():
+    """A prompt alone, and behind another one, in one kernel: the same tiles, the same bits."""
+    s = Setup([(400, 400), (400, 1000)], 2, 128, 32, seed=24)
+    q = s.draw(8, "bf16")
+    both = kv.attention(q, s.cache, s.batch)
+    one = kv.attention(q[400:], s.cache, kv.Batch(torch.tensor([0, 400], dtype=torch.int32, device=DEV),
+                                                  s.batch.context[1:], s.batch.table[1:], max_tokens=400, max_context=1000))
+    assert (one.float() - both[400:].float()).abs().max() <= 2.0 ** -6 * both.float().abs().max()
