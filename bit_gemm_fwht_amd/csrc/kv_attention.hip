@@ -129,7 +129,9 @@ __device__ __forceinline__ void store_out4(void* out, int64_t at, f32x4 y) {
 // What there is to do is counted in units of a.unit keys of a tile of a kv head, sequence by sequence;
 // every workgroup takes the same number of consecutive units (a.share_min at least), wherever in a tile
 // they begin and end. However uneven the contexts, all CUs read as much: a step of 64 sequences of 4127
-// tokens on average takes 104 us so, and 126 us with one workgroup for each tile. A tile that lies
+// tokens on average (32 heads on 8 kv heads, 554 MB) takes 115 + 7 us, 4.8 TB/s, two of 131071 tokens 97 + 8
+// us, 5.5 TB/s of the 5.96 that plain reading reaches; bound by the reads and, where tiles change within a
+// share, by the latency of the next one's first keys. A tile that lies
 // within one workgroup's share is written as output. Of the others each workgroup leaves at most two
 // partial results, of the tile that its share begins in (place 0) and of the one that it ends in
 // (place 1), which k_kv_attn_join puts together.
@@ -529,6 +531,8 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a) {
 // wave multiplies with 32x32x16 instructions; as above the accumulator of S^T is, once exponentials are
 // taken, the second operand of O^T's product: 16 consecutive keys in a lane. Weights enter as sums of two
 // bf16 (fp32 queries: three), cut and rounded next to the products, where the vector unit has time.
+// A prompt of 4096 tokens and 32 heads of 128 takes 203 us, 680 TFLOP/s of attention (1020 of products),
+// bound by the vector instructions of the softmax: beside a wave that multiplies, each takes 7 to 12 clk.
 // (Weights as one fp16 each take 160 us instead of 206 for a prompt of 4096 tokens and 32 heads, but lose channels to which
 // only keys of small weight contribute: fp16 ends 2^-24 below 1.)
 // ---------------------------------------------------------------------------------------------
@@ -726,7 +730,7 @@ __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(K
     // Of eight waves the two halves (a wave of each on every SIMD) work half a step apart: while one
     // multiplies (the weights of the step before with V, then K with q), the other is at its softmax, and
     // the barriers between the halves of a step keep it so: waves of one SIMD in the same half compete
-    // for one unit and leave the other idle (166 us instead of 160 for the prompt below). In the half in
+    // for one unit and leave the other idle. In the half in
     // which they multiply the first four waves write the next step's K to LDS and the last four its V: K
     // takes the place of the K before this step's, which every wave is done with by then, and V, still
     // wanted half a step longer, has three places. (Four waves write in the other half, all at once.)
@@ -880,12 +884,14 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
     const int64_t tiles = tiles_of(kRows);
 
     // Which kernel: by the time of their steps of 64 keys, as measured. In rows of 16 a wave's step takes
-    // 3 us (2.3 to 4.6), with 4 or 8 waves on a CU at a time whatever the number of tiles, and splitting and
-    // joining take about 15 us; in tiles a workgroup goes through all of its tile's keys: a step of four
-    // waves takes 1.65 us alone on a CU, 2.4 us with a second workgroup there or with eight waves, more
-    // where a lane holds more. (4096 tokens of 32 heads: 160 us in tiles, 390 us in rows; 512 rows of one
-    // head over 32000 keys: 799 us in tiles, 52 us in rows.) Tiles are of 128 rows unless there are more
-    // of them than two for a CU.
+    // 3 us, and 4.6 us where all the keys are more than the L2s hold (64 tokens of 32 heads on 8 over 4000
+    // keys, 8 such sequences: 162 us, in tiles 135; 512 tokens of one sequence over 4096, as many rows: 103
+    // us, in tiles 137), with 4 or 8 waves on a CU at a time whatever the number of tiles, and splitting
+    // and joining take about 15 us; in tiles a workgroup goes through all of its tile's keys: a step of four
+    // waves takes 2.1 us alone on a CU, 2.7 us with a second workgroup there, one of eight waves 3.0 us, and
+    // more where a lane holds more. (4096 tokens of 32 heads: 203 us in tiles, 390 us in rows; 512 rows of
+    // one head over 32000 keys: 1.1 ms in tiles, 52 us in rows.) Tiles are of 128 rows unless there are
+    // more of them than two for a CU.
     const bool wide = tile_nw(dtype, U) == 8;  // the variants of which two workgroups fit a CU
     const int nw = wide && tiles_of(128) > 2 * cus ? 8 : 4;
     const auto steps_of = [&](int r) {
@@ -893,9 +899,10 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
         return (double)((k + 63) / 64);
     };
     const int64_t at_once = (int64_t)cus * (wide && nw == 4 ? 2 : 1), ntiles = tiles_of(32 * nw);
-    const double step_us = wide ? (nw == 4 && ntiles <= cus ? 1.65 : 2.4) : dtype == DT_BF16 ? 3.1 : U == 2 ? 3.0 : 7.6;
+    const double step_us = wide ? (nw == 8 ? 3.0 : ntiles <= cus ? 2.1 : 2.7) : dtype == DT_BF16 ? 3.9 : U == 2 ? 3.0 : 7.6;
     const double tiles_us = step_us * steps_of(32 * nw) * (double)((ntiles + at_once - 1) / at_once);
-    const double rows_us = 15.0 + 3.0 * steps_of(kRows) * (double)tiles / (4.0 * rows_waves(dtype, U) * cus);
+    const bool in_l2 = (double)c.S * c.H * (double)keys * 2.0 * c.D <= 32.0 * (1 << 20);
+    const double rows_us = 15.0 + (in_l2 ? 3.0 : 4.6) * steps_of(kRows) * (double)tiles / (4.0 * rows_waves(dtype, U) * cus);
     const int64_t slots = (int64_t)c.T * G / (32 * nw) + c.S;
     if ((int64_t)c.T * G >= 2 * kRows * (int64_t)c.S && tiles_us < rows_us && slots * c.H < (int64_t(1) << 31)) {
         p.tile_slots = (int)slots;
