@@ -446,7 +446,17 @@ __device__ __forceinline__ void attn_rows(const KvAttnArgs& a, const AttnTile& t
 template <int DT, int U, bool FULL, int NW>
 __global__ __launch_bounds__(64 * NW, rows_waves(DT, U)) void k_kv_attn_rows(KvAttnArgs a) {
     Units q = count_units(a);
-    int at = (int)blockIdx.x * q.share;
+    // Workgroups go to the XCDs in turn: where a head has several tiles, shares that follow one another
+    // stay on one XCD, so that those tiles meet in its L2 (8 sequences of 64 tokens, 32 heads on 8, over
+    // 4000 keys: 162 -> 97 us). Tiles that share no keys stay in turn (64 sequences of 4127 tokens: 121 us
+    // in turn, 127 us so).
+    int w = blockIdx.x;
+    if (a.near) {
+        const int used = (q.total + q.share - 1) / q.share, x = w & 7;
+        if (w >= used) return;
+        w = x * (used >> 3) + min(x, used & 7) + (w >> 3);
+    }
+    int at = w * q.share;
     const int stop = min(at + q.share, q.total);
     while (at < stop) {
         const UnitPlace p = find_unit(a, q, at);
@@ -456,7 +466,7 @@ __global__ __launch_bounds__(64 * NW, rows_waves(DT, U)) void k_kv_attn_rows(KvA
         const int begin = max(lo + p.u * a.unit, t.lo & ~63);
         const int end = u1 == p.units ? t.hi : min(t.hi, lo + u1 * a.unit);
         const bool whole = p.u == 0 && u1 == p.units;
-        attn_rows<DT, U, FULL, NW>(a, t, p.h, begin, end, whole ? -1 : 2 * (int)blockIdx.x + (p.u == 0));
+        attn_rows<DT, U, FULL, NW>(a, t, p.h, begin, end, whole ? -1 : 2 * w + (p.u == 0));
         at += u1 - p.u;
     }
 }
@@ -884,10 +894,8 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
     const int64_t tiles = tiles_of(kRows);
 
     // Which kernel: by the time of their steps of 64 keys, as measured. In rows of 16 a wave's step takes
-    // 3 us, and 4.6 us where all the keys are more than the L2s hold (64 tokens of 32 heads on 8 over 4000
-    // keys, 8 such sequences: 162 us, in tiles 135; 512 tokens of one sequence over 4096, as many rows: 103
-    // us, in tiles 137), with 4 or 8 waves on a CU at a time whatever the number of tiles, and splitting
-    // and joining take about 15 us; in tiles a workgroup goes through all of its tile's keys: a step of four
+    // 3 us (2.3 to 3.8), with 4 or 8 waves on a CU at a time whatever the number of tiles, and splitting and
+    // joining take about 15 us; in tiles a workgroup goes through all of its tile's keys: a step of four
     // waves takes 2.1 us alone on a CU, 2.7 us with a second workgroup there, one of eight waves 3.0 us, and
     // more where a lane holds more. (4096 tokens of 32 heads: 203 us in tiles, 390 us in rows; 512 rows of
     // one head over 32000 keys: 1.1 ms in tiles, 52 us in rows.) Tiles are of 128 rows unless there are
@@ -901,8 +909,7 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
     const int64_t at_once = (int64_t)cus * (wide && nw == 4 ? 2 : 1), ntiles = tiles_of(32 * nw);
     const double step_us = wide ? (nw == 8 ? 3.0 : ntiles <= cus ? 2.1 : 2.7) : dtype == DT_BF16 ? 3.9 : U == 2 ? 3.0 : 7.6;
     const double tiles_us = step_us * steps_of(32 * nw) * (double)((ntiles + at_once - 1) / at_once);
-    const bool in_l2 = (double)c.S * c.H * (double)keys * 2.0 * c.D <= 32.0 * (1 << 20);
-    const double rows_us = 15.0 + (in_l2 ? 3.0 : 4.6) * steps_of(kRows) * (double)tiles / (4.0 * rows_waves(dtype, U) * cus);
+    const double rows_us = 15.0 + 3.0 * steps_of(kRows) * (double)tiles / (4.0 * rows_waves(dtype, U) * cus);
     const int64_t slots = (int64_t)c.T * G / (32 * nw) + c.S;
     if ((int64_t)c.T * G >= 2 * kRows * (int64_t)c.S && tiles_us < rows_us && slots * c.H < (int64_t(1) << 31)) {
         p.tile_slots = (int)slots;
@@ -927,6 +934,7 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
         p.nw = 4;
         p.unit = (int)unit;
         p.share_min = 2;
+        p.near = (int64_t)c.T * G > kRows * (int64_t)c.S;
         p.grid = cus * waves;
         p.join_rows = (int)std::min<int64_t>(max_tokens > 0 ? (int64_t)max_tokens * G : kRows, kRows);
         p.ws = (int64_t)p.grid * 2 * kRows * (c.D + 2) * 4;
@@ -980,6 +988,7 @@ hipError_t launch_kv_attention(KvAttnArgs a, const KvAttnPlan& p, int dtype, voi
     a.grid = p.grid;
     a.unit = p.unit;
     a.share_min = p.share_min;
+    a.near = p.near;
     a.part_o = reinterpret_cast<float*>(ws);
     a.part_ml = a.part_o + (int64_t)p.grid * 2 * kRows * a.c.D;
     return dtype == DT_BF16 ? launch_dt<DT_BF16>(a, p, s) : launch_dt<DT_F32>(a, p, s);

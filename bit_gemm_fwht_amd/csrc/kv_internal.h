@@ -45,6 +45,7 @@ struct KvAttnArgs {
     int grid;          // workgroups of the kernel for few rows
     int unit;          // keys that work is counted in, a multiple of 64 (16 rows)
     int share_min;     // units of a workgroup, at least
+    bool near;         // shares that follow one another go to the same XCD
     float* part_o;     // [grid][2][16][D] unnormalised outputs of tiles that workgroups share
     float* part_ml;    // [grid][2][16][2] maximum (log2 units) and sum
 };
@@ -56,6 +57,7 @@ hipError_t launch_kv_read(const KvRowsArgs& a, int dtype, hipStream_t s);
 struct KvAttnPlan {
     int tile_slots;  // row tiles of the kernel for many rows, 0: the kernel for few
     int grid, unit, share_min, nw;
+    bool near;
     int join_rows;  // rows of a tile that can be split, 0: no tile is
     int64_t ws;     // bytes of workspace
 };
