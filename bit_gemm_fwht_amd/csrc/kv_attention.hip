@@ -471,13 +471,14 @@ __global__ __launch_bounds__(64 * NW, rows_waves(DT, U)) void k_kv_attn_rows(KvA
     }
 }
 
-// The partial results of a row's key splits joined: workgroup (r, w) for row r of the tile that share w
-// ends in, if it begins there too. Its threads take 4 channels each and the splits in turn (all loads
-// of a thread are independent of one another), then join over LDS, always in the same order.
+// The partial results of a row's key splits joined: workgroups (., w) for the tile that share w ends in, if
+// it begins there too, a row each and the others of its rows in turn (as many workgroups as a tile is
+// promised to have rows; it may have more). A workgroup's threads take 4 channels each and the splits in
+// turn (all loads of a thread are independent of one another), then join over LDS, always in the same order.
 template <int DT>
 __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a) {
     const KvView& c = a.c;
-    const int rr = blockIdx.x, w = blockIdx.y, D = c.D;
+    const int w = blockIdx.y, D = c.D;
     Units q = count_units(a);
     const int cut = (w + 1) * q.share;
     if (cut >= q.total) return;
@@ -485,54 +486,58 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a) {
     const int first = cut - p.u;
     if (p.u == 0 || first < w * q.share) return;
     const AttnTile t = attn_tile<kRows>(a, p.s, p.tile);
-    if (rr >= t.r1 - t.r0) return;
     const int h = p.h, splits = (first + p.units - 1) / q.share - w + 1;
-    // row of split z: place 1 of share w, then place 0 of those after it
-    const auto row = [&](int z) { return ((int64_t)(2 * (w + z)) + (z == 0)) * kRows + rr; };
     const int tid = threadIdx.x;
+    const int per = D >> 2, lanes = 256 / per;  // threads of one split; splits at once
+    const int mine = tid / per, d = (tid - mine * per) * 4;
     __shared__ float sf[256];  // each split's factor exp2(m_z - m), 256 splits at a time
     __shared__ float sm[4];
     __shared__ f32x4 so[256];
-    float m = kNegInf;
-    for (int z = tid; z < splits; z += 256) m = fmaxf(m, a.part_ml[2 * row(z)]);
+#pragma unroll 1
+    for (int rr = blockIdx.x; rr < t.r1 - t.r0; rr += gridDim.x) {
+        // row of split z: place 1 of share w, then place 0 of those after it
+        const auto row = [&](int z) { return ((int64_t)(2 * (w + z)) + (z == 0)) * kRows + rr; };
+        float m = kNegInf;
+        for (int z = tid; z < splits; z += 256) m = fmaxf(m, a.part_ml[2 * row(z)]);
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if ((tid & 63) == 0) sm[tid >> 6] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    const float ms = m == kNegInf ? 0.0f : m;
+        for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+        if ((tid & 63) == 0) sm[tid >> 6] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+        const float ms = m == kNegInf ? 0.0f : m;
 
-    const int per = D >> 2, lanes = 256 / per;  // threads of one split; splits at once
-    const int mine = tid / per, d = (tid - mine * per) * 4;
-    float l = 0.0f;
-    f32x4 o = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    for (int z0 = 0; z0 < splits; z0 += 256) {
-        const int n = min(256, splits - z0);
-        __syncthreads();
-        if (tid < n) {
-            const float* ml = a.part_ml + 2 * row(z0 + tid);
-            const float f = __builtin_amdgcn_exp2f(ml[0] - ms);
-            sf[tid] = f;
-            l += ml[1] * f;
-        }
-        __syncthreads();
-        if (mine < lanes) {
+        float l = 0.0f;
+        f32x4 o = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int z0 = 0; z0 < splits; z0 += 256) {
+            const int n = min(256, splits - z0);
+            __syncthreads();
+            if (tid < n) {
+                const float* ml = a.part_ml + 2 * row(z0 + tid);
+                const float f = __builtin_amdgcn_exp2f(ml[0] - ms);
+                sf[tid] = f;
+                l += ml[1] * f;
+            }
+            __syncthreads();
+            if (mine < lanes) {
 #pragma unroll 4
-            for (int z = mine; z < n; z += lanes)
-                o += *reinterpret_cast<const f32x4*>(a.part_o + row(z0 + z) * D + d) * sf[z];
+                for (int z = mine; z < n; z += lanes)
+                    o += *reinterpret_cast<const f32x4*>(a.part_o + row(z0 + z) * D + d) * sf[z];
+            }
         }
-    }
-    so[tid] = o;
+        so[tid] = o;
 #pragma unroll
-    for (int i = 1; i < 64; i <<= 1) l += __shfl_xor(l, i);
-    if ((tid & 63) == 0) sm[tid >> 6] = l;  // every thread has read sm's maxima: two barriers since
-    __syncthreads();
-    l = (sm[0] + sm[1]) + (sm[2] + sm[3]);
-    if (mine != 0) return;
-    for (int i = 1; i < lanes; ++i) o += so[i * per + tid];
-    const int r = t.r0 + rr, tok = r / a.G, head = h * a.G + r - tok * a.G;
-    store_out4<DT>(a.out, (int64_t)(t.tok0 + tok) * a.ldo + (int64_t)head * a.ldo_head + d, o * safe_rcp(l));
-    if (a.lse && d == 0) a.lse[(int64_t)(t.tok0 + tok) * a.Hq + head] = lse_of(m, l);
+        for (int i = 1; i < 64; i <<= 1) l += __shfl_xor(l, i);
+        if ((tid & 63) == 0) sm[tid >> 6] = l;  // every thread has read sm's maxima: two barriers since
+        __syncthreads();
+        if (mine == 0) {
+            l = (sm[0] + sm[1]) + (sm[2] + sm[3]);
+            for (int i = 1; i < lanes; ++i) o += so[i * per + tid];
+            const int r = t.r0 + rr, tok = r / a.G, head = h * a.G + r - tok * a.G;
+            store_out4<DT>(a.out, (int64_t)(t.tok0 + tok) * a.ldo + (int64_t)head * a.ldo_head + d, o * safe_rcp(l));
+            if (a.lse && d == 0) a.lse[(int64_t)(t.tok0 + tok) * a.Hq + head] = lse_of(m, l);
+        }
+        __syncthreads();  // sm and so are the next row's
+    }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -936,6 +941,7 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
         p.share_min = 2;
         p.near = (int64_t)c.T * G > kRows * (int64_t)c.S;
         p.grid = cus * waves;
+        // (workgroups of the join for a tile: its rows, if the hint holds; each goes on to further rows)
         p.join_rows = (int)std::min<int64_t>(max_tokens > 0 ? (int64_t)max_tokens * G : kRows, kRows);
         p.ws = (int64_t)p.grid * 2 * kRows * (c.D + 2) * 4;
     }

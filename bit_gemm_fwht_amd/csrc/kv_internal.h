@@ -58,7 +58,7 @@ struct KvAttnPlan {
     int tile_slots;  // row tiles of the kernel for many rows, 0: the kernel for few
     int grid, unit, share_min, nw;
     bool near;
-    int join_rows;  // rows of a tile that can be split, 0: no tile is
+    int join_rows;  // workgroups of the join for each share, 0: no tile is split
     int64_t ws;     // bytes of workspace
 };
 KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int max_tokens, int max_context);
