@@ -310,7 +310,8 @@ __device__ __forceinline__ void attn_rows(const KvAttnArgs& a, const AttnTile& t
         // (loads return in order: asked for after V, the pages and the scales would wait for it)
         const int ek = entry_of(tk_next), ev = entry_of(tv_next);
         const int64_t sb = (int64_t)max(pv, 0) * c.H + h;
-        const uint32_t ks = c.ks[sb], vs = c.vs[sb];
+        const uint32_t ks = c.ks[sb];
+        uint32_t vs = c.vs[sb];
         __builtin_amdgcn_sched_barrier(0);
         const uint8_t* vp = c.vc + (((int64_t)max(pv, 0) * c.H + h) * D + li) * P + (tv & (P - 1));
 #pragma unroll
@@ -345,7 +346,9 @@ __device__ __forceinline__ void attn_rows(const KvAttnArgs& a, const AttnTile& t
                 const int key = tv + i;
                 if (!(pv >= 0 && key >= row_lo && key < row_hi)) s[i] = kNegInf;
             }
-            // V where no row may attend is whatever memory held: made zero, as 0 * NaN is not 0
+            // V where no row may attend is whatever memory held: made zero, as 0 * NaN is not 0; and so is
+            // the scale of a block of which no row may attend any key (code 255 would make 0 * inf)
+            if (pv < 0 || tv >= t.hi || tv + 16 <= t.lo) vs = 127;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int n1 = pv < 0 ? 0 : min(max(t.hi - tv - 4 * j, 0), 4), n0 = min(max(t.lo - tv - 4 * j, 0), 4);
@@ -605,10 +608,12 @@ struct TileStager {
         for (int u = 0; u < U; ++u) raw[u] = *reinterpret_cast<const u32x4*>(p + (FULL || 64 * u + need < D ? (int)(u * at_u) : -(int)at));
     }
     __device__ __forceinline__ void stage(int D, const AttnTile& t, int kb, int buf, int* some, int id) {
-        const float scale = e8m0_value(code);
+        float scale = e8m0_value(code);
         if (is_v) {
             const int tv = kb + tok;
-            if (kb < t.lo || kb + kTileKeys > t.hi || __ballot(!there)) {  // what no row may attend is made zero
+            if (kb < t.lo || kb + kTileKeys > t.hi || __ballot(!there)) {
+                // what no row may attend is made zero, and its block's scale one (0 * inf is not 0)
+                if (!there || tv + 16 <= t.lo) scale = 1.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int n1 = there ? min(max(t.hi - tv - 4 * j, 0), 4) : 0, n0 = min(max(t.lo - tv - 4 * j, 0), 4);

@@ -13,21 +13,24 @@ from test_gpu_kv import DEV, DT, Setup, host
 pytestmark = pytest.mark.gpu
 
 
-def bounds(dtype, absv, mag, cnt, out):
-    """How far out and lse may be from the exact ones.
+def bounds(dtype, absv, mag, cnt):
+    """How far out may be from the exact one before it is rounded to its type, and lse.
     Scores: products with K are exact; D <= 256 additions and the scale err by 2^-23 of sum |q k| each at
     most (the matrix core's additions taken as no better than truncating): es = 258 * 2^-23 * mag. A
     score's difference to the maximum in log2 units is rounded once (2^-23 * 2 mag) and the exponential is
     good to 2 ulp: a weight is off by a factor 1 +- (2 es + 2^-21 mag + 2^-21). A sum of n weights errs by
     n * 2^-23 of the sum of their sizes, numerator and denominator alike, rescales included. bf16 queries:
     weights are sums of two bf16, the first cut after 8 significant bits (the rest is below 2^-7 of the
-    weight's power of two), the second rounded to 8 (2^-16 of it): 2^-16, numerator only; and the output
-    is rounded (2^-9). fp32 queries: three bf16, exact; one rounding of the output."""
+    weight's power of two), the second rounded to 8 (2^-16 of it): 2^-16, numerator only. fp32 queries:
+    three bf16, exact."""
     es = 258 * 2.0 ** -23 * mag
     w = 2 * es + 2.0 ** -21 * mag + 2.0 ** -21 + cnt * 2.0 ** -23
     rel = 2 * w[..., None] + (2.0 ** -16 if dtype == "bf16" else 0.0)
-    tol = rel * absv * 1.01 + np.abs(out) * (2.0 ** -9 * 1.01 if dtype == "bf16" else 2.0 ** -22) + 1e-37
-    return tol, w + 2.0 ** -22 * (1 + mag + np.log(np.maximum(cnt, 1)))
+    return rel * absv * 1.01 + 1e-37, w + 2.0 ** -22 * (1 + mag + np.log(np.maximum(cnt, 1)))
+
+
+def rounded(x, dtype):
+    return torch.from_numpy(x).to(torch.float32).to(DT[dtype]).to(torch.float64).numpy()
 
 
 def check(s, q_heads, dtype, causal=True, window=0, scale=None, q=None, kv_heads=None):
@@ -47,9 +50,12 @@ def check(s, q_heads, dtype, causal=True, window=0, scale=None, q=None, kv_heads
     bad = (~torch.isfinite(out)).any(2) | torch.isnan(lse)
     assert not bad.any().item(), f"{int(bad.sum())} of {bad.numel()} rows, (token, head) {bad.nonzero()[0].tolist()} first"
     o, got = host(out)[:, hq], host(lse)[:, hq]
-    tol, ltol = bounds(dtype, absv, mag, cnt, eo)
-    err, none = np.abs(o - eo), cnt == 0
-    assert (err <= tol).all(), f"worst excess {(err / tol).max():.3g}"
+    tol, ltol = bounds(dtype, absv, mag, cnt)
+    # rounding keeps the order: out lies between the rounded ends of what it may have been before
+    lo, hi = rounded(eo - tol, dtype), rounded(eo + tol, dtype)
+    wrong = (o < lo) | (o > hi)
+    assert not wrong.any(), f"{wrong.sum()} of {wrong.size} off, up to {(np.abs(o - eo) / tol)[wrong].max():.3g} bounds"
+    none = cnt == 0
     assert np.array_equal(np.isneginf(got), none) and not o[none].any()
     assert (np.abs(got[~none] - el[~none]) <= ltol[~none]).all()
     return out
@@ -67,3 +73,59 @@ def test_hints_that_are_too_small_leave_no_row_unwritten(lens, heads, group, hin
     s = Setup(lens, heads, 64, 32, seed=30)
     s.batch = kv.Batch(s.batch.cu_tokens, s.batch.context, s.batch.table, max_tokens=hint[0], max_context=hint[1])
     check(s, heads * group, dtype)
+
+
+# --------------------------------------------------------------------- places that hold nothing
+def poison_scales(s, code=255):
+    """Every scale of a page that holds no token of the batch, page 0's among them (the page that stands in
+    for one that is missing), set to `code`."""
+    used = {int(p) for i, n in enumerate(s.need) for p in s.table[i, :n] if 0 <= p < s.ref.pages}
+    free = [p for p in range(s.ref.pages) if p not in used]
+    if 0 in used:  # page 0 changes places with a free one
+        f = free[0]
+        s.table[s.table == 0] = f
+        for a in (s.ref.k, s.ref.v, s.ref.ks, s.ref.vs):
+            a[f] = a[0]
+        free[0] = 0
+        s.batch.table.copy_(torch.from_numpy(s.table))
+    s.ref.ks[free], s.ref.vs[free] = code, code
+    s.ref.k[free], s.ref.v[free] = 0x7F, 0xFF
+    for t, a in ((s.cache.k_codes, s.ref.k), (s.cache.v_codes, s.ref.v), (s.cache.k_scales, s.ref.ks),
+                 (s.cache.v_scales, s.ref.vs)):
+        t.copy_(torch.from_numpy(a))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,heads,group,dim,page", [
+    ([(1, 37), (3, 100), (2, 1000)], 2, 3, 64, 16),       # few rows
+    ([(1, 5000), (2, 4000)], 2, 4, 128, 32),              # split over the chip
+    ([(700, 700), (300, 900)], 8, 8, 64, 16),             # many rows
+    ([(300, 800)], 32, 8, 64, 64),                        # many rows, enough tiles for eight waves
+])
+def test_scales_of_places_without_a_token_are_not_used(lens, heads, group, dim, page, dtype):
+    """Pages that are missing in the middle of a context, and pages wholly before a window, under scale
+    codes of 255 (not a number)."""
+    s = Setup(lens, heads, dim, page, seed=31, fill=0x7F)
+    poison_scales(s)
+    hs = [0, heads - 1]
+    check(s, heads * group, dtype, kv_heads=hs)
+    at = [min(n - 1, 2 + 3 * i) for i, n in enumerate(s.need)]
+    gone = [int(s.table[i, j]) for i, j in enumerate(at)]
+    for i, j in enumerate(at):
+        s.table[i, j] = [-1, s.ref.pages, 1 << 30][i % 3]
+    s.batch.table.copy_(torch.from_numpy(s.table))
+    s.ref.ks[gone], s.ref.vs[gone] = 255, 255  # nobody's now
+    s.cache.k_scales.copy_(torch.from_numpy(s.ref.ks))
+    s.cache.v_scales.copy_(torch.from_numpy(s.ref.vs))
+    for scale in (None, 0.0):
+        check(s, heads * group, dtype, scale=scale, kv_heads=hs)
+    # pages before every window belong to nobody either, but stay in the table
+    window = 70
+    before = [int(p) for i, (n, ctx) in enumerate(lens) for p in s.table[i, :max(0, ctx - n - window + 1) // page]
+              if 0 <= p < s.ref.pages]
+    s.ref.ks[before], s.ref.vs[before] = 255, 255
+    s.ref.k[before], s.ref.v[before] = 0x7F, 0x7F
+    for t, a in ((s.cache.k_codes, s.ref.k), (s.cache.v_codes, s.ref.v), (s.cache.k_scales, s.ref.ks),
+                 (s.cache.v_scales, s.ref.vs)):
+        t.copy_(torch.from_numpy(a))
+    check(s, heads * group, dtype, window=window, kv_heads=hs)
