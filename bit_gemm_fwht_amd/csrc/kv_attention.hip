@@ -86,6 +86,10 @@ struct AttnTile {
     int flo, fhi;     // keys that every row may attend
 };
 
+// First key in the window of the query at position pos; below 0: every key is. (A query before the first
+// token sees what the one at -1 sees: pos - window itself need not fit 32 bits.)
+__device__ __forceinline__ int window_from(int pos, int window) { return max(pos, -1) - window + 1; }
+
 template <int TR>
 __device__ __forceinline__ AttnTile attn_tile(const KvAttnArgs& a, int s, int tile) {
     const KvView& c = a.c;
@@ -101,8 +105,8 @@ __device__ __forceinline__ AttnTile attn_tile(const KvAttnArgs& a, int s, int ti
     const int pa = t.p0 + t.r0 / a.G, pb = t.p0 + (t.r1 - 1) / a.G;  // positions of the first and last row
     t.hi = a.causal ? max(min(t.keys, pb + 1), 0) : t.keys;
     t.fhi = a.causal ? min(t.keys, pa + 1) : t.keys;
-    t.lo = a.window ? max(pa - a.window + 1, 0) : 0;
-    t.flo = a.window ? pb - a.window + 1 : 0;
+    t.lo = a.window ? max(window_from(pa, a.window), 0) : 0;
+    t.flo = a.window ? window_from(pb, a.window) : 0;
     return t;
 }
 
@@ -143,7 +147,7 @@ __device__ __forceinline__ int seq_units(const KvAttnArgs& a, int s, int* tiles,
     const KvView& c = a.c;
     const int n = cu_at(c, s + 1) - cu_at(c, s), ctx = max(c.ctx[s], 0);
     const int keys = (int)min((int64_t)ctx, (int64_t)c.W << c.pshift);
-    const int lo = a.window ? max(ctx - n - a.window + 1, 0) & ~63 : 0;
+    const int lo = a.window ? max(window_from(ctx - n, a.window), 0) & ~63 : 0;
     *tiles = max(n * a.G + kRows - 1, 0) / kRows;
     *units = keys > lo ? (keys - lo + a.unit - 1) / a.unit : 1;
     return c.H * *tiles * *units;
@@ -226,7 +230,7 @@ __device__ __forceinline__ void attn_rows(const KvAttnArgs& a, const AttnTile& t
     const int head = h * a.G + (row_ok ? r - tok * a.G : 0);
     const int pos = t.p0 + tok;
     const int row_hi = !row_ok ? 0 : a.causal ? min(t.keys, pos + 1) : t.keys;
-    const int row_lo = a.window ? pos - a.window + 1 : 0;
+    const int row_lo = a.window ? window_from(pos, a.window) : 0;
     f32x4 o[4 * U];
 #pragma unroll
     for (int i = 0; i < 4 * U; ++i) o[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -465,7 +469,7 @@ __global__ __launch_bounds__(64 * NW, rows_waves(DT, U)) void k_kv_attn_rows(KvA
         const UnitPlace p = find_unit(a, q, at);
         const int u1 = min(p.units, p.u + stop - at);
         const AttnTile t = attn_tile<kRows>(a, p.s, p.tile);
-        const int lo = a.window ? max(t.p0 - a.window + 1, 0) & ~63 : 0;  // where the sequence's units begin
+        const int lo = a.window ? max(window_from(t.p0, a.window), 0) & ~63 : 0;  // where the sequence's units begin
         const int begin = max(lo + p.u * a.unit, t.lo & ~63);
         const int end = u1 == p.units ? t.hi : min(t.hi, lo + u1 * a.unit);
         const bool whole = p.u == 0 && u1 == p.units;
@@ -697,11 +701,11 @@ __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(K
     const bool ok = r < t.r1;
     const int tok = ok ? r / a.G : 0, head = h * a.G + (ok ? r - tok * a.G : 0), pos = t.p0 + tok;
     const int row_hi = !ok ? 0 : a.causal ? min(t.keys, pos + 1) : t.keys;
-    const int row_lo = a.window ? pos - a.window + 1 : 0;
+    const int row_lo = a.window ? window_from(pos, a.window) : 0;
     const int ra = t.r0 + 32 * wave, rb = min(ra + 32, t.r1) - 1;
     const int pa = t.p0 + ra / a.G, pb = t.p0 + rb / a.G;
-    const int w_hi = ra > rb ? 0 : a.causal ? min(t.keys, pb + 1) : t.keys, w_lo = a.window ? pa - a.window + 1 : 0;
-    const int w_fhi = a.causal ? min(t.keys, pa + 1) : t.keys, w_flo = a.window ? pb - a.window + 1 : 0;
+    const int w_hi = ra > rb ? 0 : a.causal ? min(t.keys, pb + 1) : t.keys, w_lo = a.window ? window_from(pa, a.window) : 0;
+    const int w_fhi = a.causal ? min(t.keys, pa + 1) : t.keys, w_flo = a.window ? window_from(pb, a.window) : 0;
     bf16x8 qf[NS][4 * U];
     {
         const int64_t q0 = (int64_t)(t.tok0 + tok) * a.ldq + (int64_t)head * a.ldq_head;

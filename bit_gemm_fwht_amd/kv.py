@@ -27,6 +27,7 @@ from .fp4 import DT_BF16, DT_F32, SCALE_E8M0_CEIL, SCALE_E8M0_FLOOR, Fp4Error, s
 # The current stream's handle by device index; the public way to it makes a Stream object first, which
 # takes a third of a small call's time on the host.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_NO_WINDOW = 2 ** 31 - 1  # no position is as far back: the same as any larger window
 _CODES = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
 
 
@@ -199,7 +200,7 @@ def attention_workspace_bytes(cache: KVCache, batch: Batch, tokens: int, q_heads
                               window: int = 0) -> int:
     """Bytes of workspace attention() needs for q [tokens, q_heads, head_dim]."""
     _use(cache, batch, tokens)
-    a = AttnC(None, None, None, 0, 0, 0, 0, _CODES[dtype], q_heads, 1, window, 1.0)
+    a = AttnC(None, None, None, 0, 0, 0, 0, _CODES[dtype], q_heads, 1, min(window, _NO_WINDOW), 1.0)
     n = lib().fp4_kv_attention_workspace_bytes(cache._p, batch._p, ctypes.addressof(a))
     if n < 0:
         raise Fp4Error(fp4.ERR_INVALID_ARG, "fp4_kv_attention_workspace_bytes")
@@ -226,7 +227,7 @@ def attention(q: torch.Tensor, cache: KVCache, batch: Batch, scale: float | None
         fp4._on(dev, lse)
     _use(cache, batch, tokens)
     a = AttnC(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None, q.stride(0), q.stride(1),
-              out.stride(0), out.stride(1), code, heads, causal, window,
+              out.stride(0), out.stride(1), code, heads, causal, min(window, _NO_WINDOW),
               scale if scale is not None else 1.0 / math.sqrt(dim))
     pa = ctypes.addressof(a)
     L = lib()

@@ -129,3 +129,23 @@ def test_scales_of_places_without_a_token_are_not_used(lens, heads, group, dim, 
                  (s.cache.v_scales, s.ref.vs)):
         t.copy_(torch.from_numpy(a))
     check(s, heads * group, dtype, window=window, kv_heads=hs)
+
+
+# ------------------------------------------------------------------------------------- wide windows
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 7, 2 ** 33])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,heads,group", [
+    ([(3, 0), (0, 10), (4, 2), (2, 50), (10, 2)], 2, 3),  # rows before the first token
+    ([(10, 2), (5, 4000), (6, 3)], 2, 4),                 # beside a context that is split
+    ([(200, 150), (90, 90), (500, 400)], 8, 8),           # many rows
+])
+def test_windows_wider_than_any_context_mask_nothing(lens, heads, group, dtype, causal, window):
+    """The widest windows there are, with rows whose tokens lie before the first one: position - window
+    does not fit 32 bits."""
+    s = Setup(lens, heads, 64, 32, seed=32, fill=0x7F)
+    q = s.draw(heads * group, dtype)
+    hs = [0, heads - 1]
+    out = check(s, heads * group, dtype, causal=causal, window=window, q=q, kv_heads=hs)
+    plain = check(s, heads * group, dtype, causal=causal, q=q, kv_heads=hs)
+    assert torch.equal(out, plain)
