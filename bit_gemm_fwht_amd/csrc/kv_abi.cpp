@@ -92,6 +92,7 @@ int attn_args(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv
     const int rc = check_batch(cache, batch, &a->c);
     if (rc != FP4_OK) return rc;
     if (!t) return FP4_ERR_INVALID_ARG;
+    if ((int64_t)batch->table_pages * cache->page_tokens > kMaxKeys) return FP4_ERR_UNSUPPORTED;
     if (t->dtype != FP4_DT_F32 && t->dtype != FP4_DT_BF16) return FP4_ERR_INVALID_ARG;
     if (t->q_heads <= 0 || t->q_heads % cache->kv_heads || t->window < 0 || !std::isfinite(t->scale))
         return FP4_ERR_INVALID_ARG;

@@ -82,7 +82,7 @@ struct AttnTile {
     int r0, r1;       // its rows [r0, r1) of n * G
     int p0;           // position of the sequence's first row
     int keys;         // keys that exist: min(context, table)
-    int lo, hi;       // keys that some row may attend
+    int lo, hi;       // keys that some row may attend (lo: past the keys where windows are)
     int flo, fhi;     // keys that every row may attend
 };
 
@@ -142,12 +142,17 @@ __device__ __forceinline__ void store_out4(void* out, int64_t at, f32x4 y) {
 // ---------------------------------------------------------------------------------------------
 constexpr int kRows = 16;
 
+// the key that a sequence's units begin at; p0: position of its first row
+__device__ __forceinline__ int units_from(const KvAttnArgs& a, int p0, int keys) {
+    return a.window ? min(max(window_from(p0, a.window), 0), keys) & ~63 : 0;
+}
+
 // tiles of a sequence, units of each of them, and its units in all
 __device__ __forceinline__ int seq_units(const KvAttnArgs& a, int s, int* tiles, int* units) {
     const KvView& c = a.c;
     const int n = cu_at(c, s + 1) - cu_at(c, s), ctx = max(c.ctx[s], 0);
     const int keys = (int)min((int64_t)ctx, (int64_t)c.W << c.pshift);
-    const int lo = a.window ? max(window_from(ctx - n, a.window), 0) & ~63 : 0;
+    const int lo = units_from(a, ctx - n, keys);
     *tiles = max(n * a.G + kRows - 1, 0) / kRows;
     *units = keys > lo ? (keys - lo + a.unit - 1) / a.unit : 1;
     return c.H * *tiles * *units;
@@ -469,8 +474,8 @@ __global__ __launch_bounds__(64 * NW, rows_waves(DT, U)) void k_kv_attn_rows(KvA
         const UnitPlace p = find_unit(a, q, at);
         const int u1 = min(p.units, p.u + stop - at);
         const AttnTile t = attn_tile<kRows>(a, p.s, p.tile);
-        const int lo = a.window ? max(window_from(t.p0, a.window), 0) & ~63 : 0;  // where the sequence's units begin
-        const int begin = max(lo + p.u * a.unit, t.lo & ~63);
+        const int lo = units_from(a, t.p0, t.keys);
+        const int begin = min(max(lo + p.u * a.unit, t.lo & ~63), kMaxKeys);
         const int end = u1 == p.units ? t.hi : min(t.hi, lo + u1 * a.unit);
         const bool whole = p.u == 0 && u1 == p.units;
         attn_rows<DT, U, FULL, NW>(a, t, p.h, begin, end, whole ? -1 : 2 * w + (p.u == 0));
@@ -691,7 +696,7 @@ __global__ __launch_bounds__(64 * NW, tile_nw(DT, U) / 4) void k_kv_attn_tiles(K
         for (int i = 0; i < NB; ++i) st[i].stage(D, t, kb, st[i].is_v ? vbuf : buf, &there[0][0], id);
     };
 
-    int kb = t.lo & ~(kTileKeys - 1);
+    int kb = min(t.lo, t.keys) & ~(kTileKeys - 1);
     entries(kb);
     load(kb);
     entries(kb + kTileKeys);

@@ -6,6 +6,10 @@
 
 namespace bgf {
 
+// Tokens of a table at most, in attention: keys are counted in 32 bits, and pages are looked up a few
+// steps past the last one.
+constexpr int kMaxKeys = 0x7FFFF000;
+
 // Cache and batch of one call (layouts in include/fp4.h).
 struct KvView {
     uint8_t* kc;

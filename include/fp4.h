@@ -356,7 +356,8 @@ int fp4_kv_read(const fp4_kv_cache* cache, const fp4_kv_batch* batch, void* k, i
  * p (its row's token, above) key j is allowed iff 0 <= j < context, (causal != 0) j <= p and
  * (window > 0) j > p - window, and
  *   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale * q.k_j),  lse = ln sum_j w_j
- * over the allowed keys; a row with none gives zeros and lse = -inf. What the cache holds in places
+ * over the allowed keys; a row with none gives zeros and lse = -inf. Tables of more than 2^31 - 4096
+ * tokens (table_pages * page_tokens) are not supported. What the cache holds in places
  * that are not allowed for any query of a sequence (past its context, pages before every window)
  * is never used, whatever its bits. Scores, softmax statistics and sums are fp32; with fp32 q, q and
  * the weights enter the matrix products as exact sums of three bf16, with bf16 q the weights as sums

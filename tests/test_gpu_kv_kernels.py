@@ -149,3 +149,19 @@ def test_windows_wider_than_any_context_mask_nothing(lens, heads, group, dtype, 
     out = check(s, heads * group, dtype, causal=causal, window=window, q=q, kv_heads=hs)
     plain = check(s, heads * group, dtype, causal=causal, q=q, kv_heads=hs)
     assert torch.equal(out, plain)
+
+
+# ------------------------------------------------------------------------------------ long contexts
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [0, 1, 50, 10000])
+@pytest.mark.parametrize("n,heads,group", [(3, 2, 4), (500, 8, 8)])
+def test_contexts_past_their_table(n, heads, group, window, dtype):
+    """A context far past what its table holds: the table's keys are all there is, positions lie behind
+    them (and windows with them)."""
+    s = Setup([(n, 1000), (2, 3000)], heads, 64, 32, seed=34, fill=0x7F)
+    for ctx in (2 ** 31 - 1, 1100):
+        s.context[0] = ctx
+        s.table[0, 31] = -1  # tokens 992 on
+        s.batch.context.copy_(torch.from_numpy(s.context))
+        s.batch.table.copy_(torch.from_numpy(s.table))
+        check(s, heads * group, dtype, window=window, kv_heads=[0])
