@@ -130,8 +130,8 @@ __device__ __forceinline__ void store_out4(void* out, int64_t at, f32x4 y) {
 // Few rows: tiles of 16, the keys dealt to the waves in steps of 64 each, straight from memory to
 // registers (no two waves read the same key).
 //
-// What there is to do is counted in units of a.unit keys of a tile of a kv head, sequence by sequence;
-// every workgroup takes the same number of consecutive units (a.share_min at least), wherever in a tile
+// What there is to do is counted in units of a.unit keys of a tile of a kv head (2^31: of whole tiles),
+// sequence by sequence; every workgroup takes the same number of consecutive units (a.share_min at least), wherever in a tile
 // they begin and end. However uneven the contexts, all CUs read as much: a step of 64 sequences of 4127
 // tokens on average (32 heads on 8 kv heads, 554 MB) takes 115 + 7 us, 4.8 TB/s, two of 131071 tokens 97 + 8
 // us, 5.5 TB/s of the 5.96 that plain reading reaches; bound by the reads and, where tiles change within a
@@ -141,6 +141,7 @@ __device__ __forceinline__ void store_out4(void* out, int64_t at, f32x4 y) {
 // (place 1), which k_kv_attn_join puts together.
 // ---------------------------------------------------------------------------------------------
 constexpr int kRows = 16;
+constexpr uint32_t kWholeTiles = 1u << 31;  // a unit that no tile has two of
 
 // the key that a sequence's units begin at; p0: position of its first row
 __device__ __forceinline__ int units_from(const KvAttnArgs& a, int p0, int keys) {
@@ -154,7 +155,7 @@ __device__ __forceinline__ int seq_units(const KvAttnArgs& a, int s, int* tiles,
     const int keys = (int)min((int64_t)ctx, (int64_t)c.W << c.pshift);
     const int lo = units_from(a, ctx - n, keys);
     *tiles = max(n * a.G + kRows - 1, 0) / kRows;
-    *units = keys > lo ? (keys - lo + a.unit - 1) / a.unit : 1;
+    *units = keys > lo ? (int)(((uint32_t)(keys - lo) + a.unit - 1) / a.unit) : 1;
     return c.H * *tiles * *units;
 }
 
@@ -475,8 +476,8 @@ __global__ __launch_bounds__(64 * NW, rows_waves(DT, U)) void k_kv_attn_rows(KvA
         const int u1 = min(p.units, p.u + stop - at);
         const AttnTile t = attn_tile<kRows>(a, p.s, p.tile);
         const int lo = units_from(a, t.p0, t.keys);
-        const int begin = min(max(lo + p.u * a.unit, t.lo & ~63), kMaxKeys);
-        const int end = u1 == p.units ? t.hi : min(t.hi, lo + u1 * a.unit);
+        const int begin = min(max(lo + p.u * (int)a.unit, t.lo & ~63), kMaxKeys);
+        const int end = u1 == p.units ? t.hi : min(t.hi, lo + u1 * (int)a.unit);
         const bool whole = p.u == 0 && u1 == p.units;
         attn_rows<DT, U, FULL, NW>(a, t, p.h, begin, end, whole ? -1 : 2 * w + (p.u == 0));
         at += u1 - p.u;
@@ -944,14 +945,14 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
         // (600 tokens of 8 kv heads: 11.7 us, in shares 13.5 + 4.2 us for the join; 64 sequences of up to
         // 2000 tokens: 41 us against 50, all of 2000: 60 us against 57).
         p.nw = 4 * waves;
-        p.unit = 1 << 30;
+        p.unit = kWholeTiles;
         p.share_min = 1;
         p.grid = (int)std::min<int64_t>(std::min(tiles, most), 1 << 30);
     } else {
         // Shares: four waves, so that a CU has a second workgroup to read for while one changes tiles or
         // joins its waves (64 sequences of 4127 tokens on average: 115 us, with one of eight 140 us).
         p.nw = 4;
-        p.unit = (int)unit;
+        p.unit = (uint32_t)unit;
         p.share_min = 2;
         p.near = (int64_t)c.T * G > kRows * (int64_t)c.S;
         p.grid = cus * waves;

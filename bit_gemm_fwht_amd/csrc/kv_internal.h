@@ -47,7 +47,7 @@ struct KvAttnArgs {
     int causal, window;
     int slots;         // row tiles of the kernel for many rows (at least those that have rows)
     int grid;          // workgroups of the kernel for few rows
-    int unit;          // keys that work is counted in, a multiple of 64 (16 rows)
+    uint32_t unit;     // keys that work is counted in, a multiple of 64 (16 rows), 2^31: whole tiles
     int share_min;     // units of a workgroup, at least
     bool near;         // shares that follow one another go to the same XCD
     float* part_o;     // [grid][2][16][D] unnormalised outputs of tiles that workgroups share
@@ -60,7 +60,8 @@ hipError_t launch_kv_read(const KvRowsArgs& a, int dtype, hipStream_t s);
 // How an attention call is cut into workgroups; the same for the size query and the launch.
 struct KvAttnPlan {
     int tile_slots;  // row tiles of the kernel for many rows, 0: the kernel for few
-    int grid, unit, share_min, nw;
+    int grid, share_min, nw;
+    uint32_t unit;
     bool near;
     int join_rows;  // workgroups of the join for each share, 0: no tile is split
     int64_t ws;     // bytes of workspace

@@ -152,6 +152,33 @@ def test_windows_wider_than_any_context_mask_nothing(lens, heads, group, dtype, 
 
 
 # ------------------------------------------------------------------------------------ long contexts
+@pytest.mark.parametrize("hint", [None, 100])
+def test_contexts_past_2_30(hint):
+    """A context of 2^30 + 3005 tokens: nearly all of its pages are one page whose keys get no weight, the
+    others lie at its start, at 2^29, on both sides of 2^30 and at its end. Split over the chip, and (as
+    the hint speaks of a short context) in one workgroup."""
+    page, dim = 128, 16
+    ctx = 2 ** 30 + 3005
+    width = -(-ctx // page)
+    at = [0, 2 ** 29 // page, 2 ** 30 // page - 1, 2 ** 30 // page, width - 1]
+    s = Setup([(1, 5 * page)], 1, dim, page, seed=33)
+    s.context[:] = 4 * page + ctx - (width - 1) * page  # the pages at `at`, for the reference
+    q = s.draw(4, "bf16")
+    q[:, :, 0] = 8.0
+    s.ref.k[..., 0] = 0
+    dull = [p for p in range(s.ref.pages) if p not in s.table[0]][0]
+    s.ref.k[dull] = 0
+    s.ref.k[dull, :, :, 0] = 0xFE  # -448
+    s.ref.ks[dull] = 127
+    for t, a in ((s.cache.k_codes, s.ref.k), (s.cache.k_scales, s.ref.ks)):
+        t.copy_(torch.from_numpy(a))
+    table = torch.full((1, width), dull, dtype=torch.int32, device=DEV)
+    table[0, at] = s.batch.table[0]
+    s.batch = kv.Batch(s.batch.cu_tokens, torch.tensor([ctx], dtype=torch.int32, device=DEV), table,
+                       max_context=hint)
+    check(s, 4, "bf16", scale=0.25, q=q)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("window", [0, 1, 50, 10000])
 @pytest.mark.parametrize("n,heads,group", [(3, 2, 4), (500, 8, 8)])
