@@ -152,6 +152,31 @@ int fp4_kv_read(const fp4_kv_cache* cache, const fp4_kv_batch* batch, void* k, i
     }
 }
 
+int fp4_kv_attention_plan(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv_attn* t, fp4_kv_plan* out) {
+    try {
+        KvAttnArgs a{};
+        KvAttnPlan p{};
+        if (!out) return FP4_ERR_INVALID_ARG;
+        const int rc = attn_args(cache, batch, t, &a, &p);
+        if (rc != FP4_OK) return rc;
+        *out = fp4_kv_plan{};
+        if (batch->tokens == 0) return FP4_OK;
+        out->waves = p.nw;
+        if (p.tile_slots) {
+            out->kernel = FP4_KV_PLAN_TILES;
+            out->tile_rows = 32 * p.nw;
+            out->workgroups = (int64_t)p.tile_slots * cache->kv_heads;
+        } else {
+            out->kernel = !p.join_rows ? FP4_KV_PLAN_ROWS : p.near ? FP4_KV_PLAN_ROWS_NEAR : FP4_KV_PLAN_ROWS_SPLIT;
+            out->tile_rows = 16;
+            out->workgroups = p.grid;
+        }
+        return FP4_OK;
+    } catch (...) {
+        return FP4_ERR_INTERNAL;
+    }
+}
+
 int64_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv_attn* t) {
     try {
         KvAttnArgs a{};

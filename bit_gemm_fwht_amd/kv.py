@@ -50,6 +50,13 @@ class AttnC(ctypes.Structure):
                 ("causal", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class PlanC(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("tile_rows", ctypes.c_int32), ("waves", ctypes.c_int32),
+                ("workgroups", ctypes.c_int64)]
+
+
+PLAN_ROWS, PLAN_ROWS_SPLIT, PLAN_ROWS_NEAR, PLAN_TILES = 1, 2, 3, 4
+
 _lib = None
 
 
@@ -64,6 +71,8 @@ def lib() -> ctypes.CDLL:
         L.fp4_kv_read.restype = ctypes.c_int
         L.fp4_kv_attention_workspace_bytes.argtypes = [P, P, P]
         L.fp4_kv_attention_workspace_bytes.restype = I64
+        L.fp4_kv_attention_plan.argtypes = [P, P, P, P]
+        L.fp4_kv_attention_plan.restype = ctypes.c_int
         L.fp4_kv_attention.argtypes = [P, P, P, P, I64, P]
         L.fp4_kv_attention.restype = ctypes.c_int
         _lib = L
@@ -207,6 +216,18 @@ def attention_workspace_bytes(cache: KVCache, batch: Batch, tokens: int, q_heads
     return n
 
 
+def attention_plan(cache: KVCache, batch: Batch, tokens: int, q_heads: int, dtype=torch.bfloat16,
+                   window: int = 0) -> PlanC:
+    """How attention() of q [tokens, q_heads, head_dim] would be carried out: kernel (PLAN_...), tile_rows,
+    waves, workgroups."""
+    _use(cache, batch, tokens)
+    a = AttnC(None, None, None, 0, 0, 0, 0, _CODES[dtype], q_heads, 1, min(window, _NO_WINDOW), 1.0)
+    p = PlanC()
+    _check(lib().fp4_kv_attention_plan(cache._p, batch._p, ctypes.addressof(a), ctypes.addressof(p)),
+           "fp4_kv_attention_plan")
+    return p
+
+
 def attention(q: torch.Tensor, cache: KVCache, batch: Batch, scale: float | None = None, causal: bool = True,
               window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
               workspace: torch.Tensor | None = None) -> torch.Tensor:
@@ -244,5 +265,5 @@ def attention(q: torch.Tensor, cache: KVCache, batch: Batch, scale: float | None
     return out
 
 
-__all__ = ["KVCache", "Batch", "empty_cache", "append", "read", "attention", "attention_workspace_bytes",
+__all__ = ["KVCache", "Batch", "empty_cache", "append", "read", "attention", "attention_plan", "attention_workspace_bytes",
            "SCALE_E8M0_CEIL", "SCALE_E8M0_FLOOR", "Fp4Error", "status_string"]

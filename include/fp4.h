@@ -377,6 +377,22 @@ typedef struct fp4_kv_attn {
     int32_t window;
     float scale;
 } fp4_kv_attn;
+/* How the call would be carried out, for profiles and tests: which kernel, the rows of a tile, the waves of a
+ * workgroup, the workgroups of the main launch. A choice of speed alone, free to change. tokens == 0:
+ * all zero. */
+enum {
+    FP4_KV_PLAN_ROWS = 1,       /* tiles of 16 rows, whole ones dealt to workgroups */
+    FP4_KV_PLAN_ROWS_SPLIT = 2, /* their keys dealt in equal shares, then joined */
+    FP4_KV_PLAN_ROWS_NEAR = 3,  /* the same, shares that follow one another on one XCD */
+    FP4_KV_PLAN_TILES = 4       /* tiles of 128 or 256 rows, keys through LDS */
+};
+typedef struct fp4_kv_plan {
+    int32_t kernel;
+    int32_t tile_rows;
+    int32_t waves;
+    int64_t workgroups;
+} fp4_kv_plan;
+int fp4_kv_attention_plan(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv_attn* a, fp4_kv_plan* plan);
 int64_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv_attn* a);
 int fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv_attn* a, void* workspace,
                      int64_t ws_bytes, void* stream);

@@ -33,9 +33,10 @@ def rounded(x, dtype):
     return torch.from_numpy(x).to(torch.float32).to(DT[dtype]).to(torch.float64).numpy()
 
 
-def check(s, q_heads, dtype, causal=True, window=0, scale=None, q=None, kv_heads=None):
+def check(s, q_heads, dtype, causal=True, window=0, scale=None, q=None, kv_heads=None, chain=None):
     """One call against the reference; what it does not write would show as NaN. kv_heads: the reference
-    looks at these only (and at their query heads)."""
+    looks at these only (and at their query heads). chain: additions that a sum goes through at most, where
+    these are fewer than its keys."""
     q = s.draw(q_heads, dtype) if q is None else q
     lse = torch.full((s.tokens, q_heads), math.nan, device=DEV)
     out = torch.full_like(q, math.nan)
@@ -50,7 +51,7 @@ def check(s, q_heads, dtype, causal=True, window=0, scale=None, q=None, kv_heads
     bad = (~torch.isfinite(out)).any(2) | torch.isnan(lse)
     assert not bad.any().item(), f"{int(bad.sum())} of {bad.numel()} rows, (token, head) {bad.nonzero()[0].tolist()} first"
     o, got = host(out)[:, hq], host(lse)[:, hq]
-    tol, ltol = bounds(dtype, absv, mag, cnt)
+    tol, ltol = bounds(dtype, absv, mag, cnt if chain is None else np.minimum(cnt, chain))
     # rounding keeps the order: out lies between the rounded ends of what it may have been before
     lo, hi = rounded(eo - tol, dtype), rounded(eo + tol, dtype)
     wrong = (o < lo) | (o > hi)
@@ -192,3 +193,160 @@ def test_contexts_past_their_table(n, heads, group, window, dtype):
         s.batch.context.copy_(torch.from_numpy(s.context))
         s.batch.table.copy_(torch.from_numpy(s.table))
         check(s, heads * group, dtype, window=window, kv_heads=[0])
+
+
+# --------------------------------------------------------------------------------- kernel by kernel
+def ragged(n, rows, longest):
+    """n sequences of 1 to `rows` rows and uneven contexts up to `longest`."""
+    return [(1 + i % rows, max(rows, round(longest * ((i + 1) * 0.6180339887 % 1.0)))) for i in range(n)]
+
+
+# name: lens, kv heads, query heads to each, dim, page, dtype, kernel, rows of a tile. Contexts of several
+# steps, tiles that end inside a sequence, dims below and at multiples of 64.
+ROWS, SPLIT, NEAR, TILES = kv.PLAN_ROWS, kv.PLAN_ROWS_SPLIT, kv.PLAN_ROWS_NEAR, kv.PLAN_TILES
+UNEVEN = [(300, 300), (500, 900), (0, 7), (129, 1640)]
+KERNELS = {
+    "rows, 70 sequences": (ragged(70, 1, 1000), 2, 4, 128, 32, "bf16", ROWS, 16),
+    "rows, 150 sequences": (ragged(150, 3, 700), 1, 5, 80, 16, "bf16", ROWS, 16),
+    "rows, 129 sequences, fp32": (ragged(129, 2, 500), 1, 3, 256, 64, "f32", ROWS, 16),
+    "split, 100 sequences": (ragged(100, 1, 5000), 2, 4, 64, 32, "bf16", SPLIT, 16),
+    "split, 80": (ragged(5, 2, 7000), 2, 3, 80, 16, "bf16", SPLIT, 16),
+    "split, 256": (ragged(3, 1, 6000), 2, 8, 256, 128, "bf16", SPLIT, 16),
+    "split, 256, fp32": (ragged(4, 1, 4000), 1, 5, 256, 16, "f32", SPLIT, 16),
+    "near, 128": ([(24, 3000), (40, 5000), (0, 3), (17, 2500)], 2, 4, 128, 32, "bf16", NEAR, 16),
+    "near, 70 sequences": (ragged(70, 9, 3000), 1, 4, 64, 64, "bf16", NEAR, 16),
+    "near, 80, fp32": ([(20, 2500), (9, 4100)], 2, 5, 80, 16, "f32", NEAR, 16),
+    "near, 256": ([(33, 3300), (5, 2600)], 1, 8, 256, 32, "bf16", NEAR, 16),
+    "eight waves, 128": ([(600, 600)], 32, 4, 128, 32, "bf16", TILES, 256),
+    "eight waves, uneven": (UNEVEN, 16, 4, 128, 16, "bf16", TILES, 256),
+    "eight waves, 64": (UNEVEN, 16, 4, 64, 64, "bf16", TILES, 256),
+    "eight waves, 48": (UNEVEN, 16, 4, 48, 128, "bf16", TILES, 256),
+    "eight waves, 112": ([(600, 600)], 32, 4, 112, 16, "bf16", TILES, 256),
+    "eight waves, 64, fp32": (UNEVEN, 16, 4, 64, 32, "f32", TILES, 256),
+    "eight waves, 32, fp32": ([(600, 700)], 32, 4, 32, 32, "f32", TILES, 256),
+    "four waves, 128": ([(700, 1500), (33, 40)], 8, 4, 128, 32, "bf16", TILES, 128),
+    "four waves, 80": ([(400, 900)], 4, 8, 80, 16, "bf16", TILES, 128),
+    "four waves, 192": ([(232, 440)], 16, 8, 192, 64, "bf16", TILES, 128),
+    "four waves, 256": ([(600, 600)], 32, 4, 256, 32, "bf16", TILES, 128),
+    "four waves, 64, fp32": ([(400, 900)], 4, 8, 64, 16, "f32", TILES, 128),
+    "four waves, 128, fp32": ([(232, 440)], 16, 8, 128, 128, "f32", TILES, 128),
+    "four waves, 176, fp32": ([(232, 380)], 16, 8, 176, 32, "f32", TILES, 128),
+    "four waves, 192, fp32": ([(232, 380)], 16, 8, 192, 16, "f32", TILES, 128),
+    "four waves, 240, fp32": ([(232, 380)], 16, 8, 240, 64, "f32", TILES, 128),
+    "four waves, 256, fp32": ([(232, 380)], 16, 8, 256, 32, "f32", TILES, 128),
+}
+
+
+def setup(name, **kw):
+    lens, heads, group, dim, page, dtype, kernel, rows = KERNELS[name]
+    s = Setup(lens, heads, dim, page, **kw)
+    return s, heads * group, dtype, [0] if heads == 1 else [0, heads - 1]
+
+
+def runs_in(s, q_heads, dtype, name, window=0):
+    """Whether the call takes the kernel that the case is meant for (as on 256 CUs)."""
+    p = kv.attention_plan(s.cache, s.batch, s.tokens, q_heads, DT[dtype], window)
+    return (p.kernel, p.tile_rows) == KERNELS[name][6:8]
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_every_kernel(name):
+    s, q_heads, dtype, hs = setup(name, seed=40, fill=0x7F)
+    assert runs_in(s, q_heads, dtype, name)
+    check(s, q_heads, dtype, kv_heads=hs)
+
+
+@pytest.mark.parametrize("causal,scale", [(False, None), (True, 0.0), (True, -0.2), (False, -0.3), (True, 2.0)])
+@pytest.mark.parametrize("name", ["rows, 150 sequences", "split, 80", "near, 128", "eight waves, uneven",
+                                  "eight waves, 64, fp32", "four waves, 80", "four waves, 192, fp32"])
+def test_every_kernel_scales_and_no_mask(name, causal, scale):
+    s, q_heads, dtype, hs = setup(name, seed=41, fill=0xFF)
+    assert runs_in(s, q_heads, dtype, name)
+    check(s, q_heads, dtype, causal=causal, scale=scale, kv_heads=hs)
+
+
+# (a window changes what a kernel costs and so the choice: here the shapes that keep theirs)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("name,window", [
+    ("rows, 70 sequences", 90), ("rows, 150 sequences", 1), ("rows, 129 sequences, fp32", 33),
+    ("split, 100 sequences", 2100), ("split, 80", 3000), ("split, 256, fp32", 2500),
+    ("near, 128", 2300), ("near, 80, fp32", 2222), ("near, 256", 2049),
+    ("eight waves, 128", 200), ("eight waves, uneven", 130), ("eight waves, 48", 1), ("eight waves, 64, fp32", 77),
+    ("four waves, 128", 300), ("four waves, 80", 65), ("four waves, 256", 100), ("four waves, 128, fp32", 150),
+])
+def test_every_kernel_windows(name, window, causal):
+    s, q_heads, dtype, hs = setup(name, seed=42, fill=0x7F)
+    assert runs_in(s, q_heads, dtype, name, window)
+    check(s, q_heads, dtype, causal=causal, window=window, kv_heads=hs)
+
+
+@pytest.mark.parametrize("name", ["rows, 70 sequences", "split, 80", "split, 256, fp32", "near, 128", "eight waves, 128",
+                                  "eight waves, uneven", "eight waves, 64, fp32", "four waves, 128", "four waves, 80",
+                                  "four waves, 256, fp32"])
+def test_every_kernel_with_pages_missing(name):
+    """Every fifth page of a table names none: past the cache, negative, in turn."""
+    s, q_heads, dtype, hs = setup(name, seed=43, fill=0x7F)
+    assert runs_in(s, q_heads, dtype, name)
+    for i, n in enumerate(s.need):
+        at = np.arange(2 + i % 3, n, 5)
+        s.table[i, at] = np.resize([-1, s.ref.pages, 1 << 30, -7], len(at))
+    s.batch.table.copy_(torch.from_numpy(s.table))
+    check(s, q_heads, dtype, kv_heads=hs)
+
+
+@pytest.mark.parametrize("low,high", [(-60, 60), (-20, 20), (-90, -90), (40, 40)])
+@pytest.mark.parametrize("name", ["rows, 70 sequences", "split, 80", "near, 128", "eight waves, uneven", "eight waves, 64, fp32",
+                                  "four waves, 80", "four waves, 240, fp32"])
+def test_every_kernel_with_blocks_of_uneven_size(name, low, high):
+    """V's block exponents far apart, and all of them far from one; blocks of zeros among them."""
+    s, q_heads, dtype, hs = setup(name, seed=44)
+    assert runs_in(s, q_heads, dtype, name)
+    r = s.ref
+    r.vs[:] = np.where(np.arange(r.pages)[:, None] % 2, 127 + high, 127 + low)
+    r.v[s.table[0, 0]] = 0
+    r.vs[s.table[0, 0]] = 0
+    s.cache.v_codes.copy_(torch.from_numpy(r.v))
+    s.cache.v_scales.copy_(torch.from_numpy(r.vs))
+    check(s, q_heads, dtype, kv_heads=hs)
+
+
+@pytest.mark.parametrize("name", ["rows, 150 sequences", "split, 80", "split, 256, fp32", "near, 128", "eight waves, uneven",
+                                  "eight waves, 64, fp32", "four waves, 80", "four waves, 192, fp32"])
+def test_weights_are_held_to_2_16(name):
+    """A quarter of the keys have weight 1 and values -1, the others weight w near 1/3 and values 1: the
+    numerator all but cancels, and weights of fewer bits would show (one bf16: 2^-9 of the sum). Shares
+    here are of 512 keys, of at most 30 to a tile."""
+    s, q_heads, dtype, hs = setup(name, seed=45)
+    assert runs_in(s, q_heads, dtype, name)
+    r = s.ref
+    r.k[:], r.v[:], r.ks[:], r.vs[:] = 0, 0x38, 127, 127
+    r.k[..., 0] = 0x38
+    r.k[:, :, ::4] = 0
+    r.v[..., ::4] = 0xB8
+    for t, a in ((s.cache.k_codes, r.k), (s.cache.v_codes, r.v), (s.cache.k_scales, r.ks), (s.cache.v_scales, r.vs)):
+        t.copy_(torch.from_numpy(a))
+    q = s.draw(q_heads, dtype)
+    q[:, :, 0] = -torch.linspace(1.0, 1.2, s.tokens * q_heads, device=DEV).view(s.tokens, q_heads).to(DT[dtype])
+    split = KERNELS[name][6] in (SPLIT, NEAR)
+    check(s, q_heads, dtype, causal=False, scale=1.0, q=q, kv_heads=hs, chain=512 + 2 + 30 if split else None)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_shares_of_a_tile_than_a_join_has_threads(dtype):
+    """293 shares of two units of 256 keys: sums go through at most 512 keys, two joins of waves and the
+    shares."""
+    s = Setup([(2, 150000)], 1, 16, 128, seed=46)
+    assert kv.attention_plan(s.cache, s.batch, 2, 4, DT[dtype]).kernel == SPLIT
+    check(s, 4, dtype, chain=512 + 2 + 293)
+
+
+def test_a_tile_gives_the_same_bits_whatever_else_is_in_the_batch():
+    """A prompt alone, and behind another one, both in tiles of 256 rows."""
+    s = Setup([(576, 576), (576, 1000)], 16, 128, 32, seed=47)
+    q = s.draw(128, "bf16")
+    one = kv.Batch(torch.tensor([0, 576], dtype=torch.int32, device=DEV), s.batch.context[1:], s.batch.table[1:],
+                   max_tokens=576, max_context=1000)
+    for b, n in ((s.batch, 1152), (one, 576)):
+        p = kv.attention_plan(s.cache, b, n, 128)
+        assert (p.kernel, p.tile_rows) == (TILES, 256)
+    assert torch.equal(kv.attention(q[576:], s.cache, one), kv.attention(q, s.cache, s.batch)[576:])

@@ -22,3 +22,37 @@ def test_tables_beyond_32_bit_keys_are_refused(kv, page):  # noqa: F811
         b = batch(kv, tokens=3, table_pages=pages, table_ld=pages)
         size, status = query(kv, cache(kv, page_tokens=page), b, attn(kv))
         assert status == want and (size == -1) == (want == fp4.ERR_UNSUPPORTED)
+
+
+def plan(kv, lens, heads, group, dim, page, dtype, window=0, **kw):  # noqa: F811
+    width = max(max(-(-c // page) for _, c in lens), 1)
+    a = dict(tokens=sum(n for n, _ in lens), table_pages=width, table_ld=width, seqs=len(lens),
+             max_tokens=max(n for n, _ in lens), max_context=max(c for _, c in lens))
+    a.update(kw)
+    p = kv.PlanC()
+    args = (cache(kv, pages=1000, kv_heads=heads, page_tokens=page, head_dim=dim), batch(kv, **a),
+            attn(kv, q_heads=heads * group, dtype=1 if dtype == "bf16" else 0, window=window), p)
+    assert kv.lib().fp4_kv_attention_plan(*(ctypes.addressof(x) for x in args)) == 0
+    return p
+
+
+def test_shapes_of_the_kernel_tests(kv):  # noqa: F811
+    """On 256 CUs (which is what is assumed where there is no GPU), the shapes that the GPU tests name after
+    kernels take them."""
+    from test_gpu_kv_kernels import KERNELS
+    for name, (lens, heads, group, dim, page, dtype, kernel, rows) in KERNELS.items():
+        p = plan(kv, lens, heads, group, dim, page, dtype)
+        assert (p.kernel, p.tile_rows) == (kernel, rows), name
+
+
+def test_plan_refuses_and_no_rows(kv):  # noqa: F811
+    from bit_gemm_fwht_amd import fp4
+    L = kv.lib()
+    p = kv.PlanC(9, 9, 9, 9)
+    c, b, a = cache(kv), batch(kv, tokens=0), attn(kv)
+    q = [ctypes.addressof(x) for x in (c, b, a)]
+    assert L.fp4_kv_attention_plan(*q, None) == fp4.ERR_INVALID_ARG
+    assert L.fp4_kv_attention_plan(*q, ctypes.addressof(p)) == fp4.OK
+    assert (p.kernel, p.tile_rows, p.waves, p.workgroups) == (0, 0, 0, 0)
+    bad = attn(kv, q_heads=3)
+    assert L.fp4_kv_attention_plan(q[0], q[1], ctypes.addressof(bad), ctypes.addressof(p)) == fp4.ERR_INVALID_ARG
