@@ -97,7 +97,7 @@ int attn_args(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv
     if (t->q_heads <= 0 || t->q_heads % cache->kv_heads || t->window < 0 || !std::isfinite(t->scale))
         return FP4_ERR_INVALID_ARG;
     const int64_t rows = batch->tokens * (t->q_heads / cache->kv_heads);
-    if (rows > kMaxRows) return FP4_ERR_UNSUPPORTED;
+    if (rows > kMaxRows || (rows / 16 + batch->seqs) * cache->kv_heads > kMaxUnits) return FP4_ERR_UNSUPPORTED;
     a->q = t->q;
     a->out = t->out;
     a->lse = t->lse;

@@ -936,11 +936,9 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
         p.nw = nw;
         return p;
     }
-    // (the kernels count units in 32 bits, whatever the hints were)
-    const int64_t most = ((int64_t)c.T * G / kRows + c.S) * c.H;
-    const int64_t unit = 256;
+    const int64_t most = ((int64_t)c.T * G / kRows + c.S) * c.H;  // tiles, whatever the hints were
     const int waves = rows_waves(dtype, U);
-    if (keys <= 2048 || most * (room / unit + 1) >= (int64_t(1) << 31)) {
+    if (keys <= 2048) {
         // Short contexts: a workgroup for each tile, of eight waves where registers allow, and one launch
         // (600 tokens of 8 kv heads: 11.7 us, in shares 13.5 + 4.2 us for the join; 64 sequences of up to
         // 2000 tokens: 41 us against 50, all of 2000: 60 us against 57).
@@ -951,8 +949,11 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
     } else {
         // Shares: four waves, so that a CU has a second workgroup to read for while one changes tiles or
         // joins its waves (64 sequences of 4127 tokens on average: 115 us, with one of eight 140 us).
+        // Units of 256 keys, or of as many more as keep their number, and the places that shares begin and
+        // end at, within 32 bits for whatever contexts the table has room for.
         p.nw = 4;
-        p.unit = (uint32_t)unit;
+        p.unit = 256;
+        while (most * (room / p.unit + 1) > kMaxUnits) p.unit *= 2;
         p.share_min = 2;
         p.near = (int64_t)c.T * G > kRows * (int64_t)c.S;
         p.grid = cus * waves;

@@ -9,6 +9,8 @@ namespace bgf {
 // Tokens of a table at most, in attention: keys are counted in 32 bits, and pages are looked up a few
 // steps past the last one.
 constexpr int kMaxKeys = 0x7FFFF000;
+// Tiles of 16 rows, and units of keys of them, in one call at most: their sums stay in 32 bits.
+constexpr int64_t kMaxUnits = int64_t(1) << 30;
 
 // Cache and batch of one call (layouts in include/fp4.h).
 struct KvView {

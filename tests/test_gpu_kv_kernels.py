@@ -340,6 +340,17 @@ def test_more_shares_of_a_tile_than_a_join_has_threads(dtype):
     check(s, 4, dtype, chain=512 + 2 + 293)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_wide_tables_are_dealt_in_larger_units(dtype):
+    """A table with room for 2^31 - 4096 tokens, 130 heads: units of 256 keys would be too many to count."""
+    s = Setup([(1, 9000)], 130, 16, 128, seed=48)
+    table = torch.full((1, 2 ** 24 - 32), -1, dtype=torch.int32, device=DEV)
+    table[:, :s.table.shape[1]] = s.batch.table
+    s.batch = kv.Batch(s.batch.cu_tokens, s.batch.context, table)
+    assert kv.attention_plan(s.cache, s.batch, 1, 260, DT[dtype]).kernel == SPLIT
+    check(s, 260, dtype, kv_heads=[0, 77, 129])
+
+
 def test_a_tile_gives_the_same_bits_whatever_else_is_in_the_batch():
     """A prompt alone, and behind another one, both in tiles of 256 rows."""
     s = Setup([(576, 576), (576, 1000)], 16, 128, 32, seed=47)

@@ -56,3 +56,21 @@ def test_plan_refuses_and_no_rows(kv):  # noqa: F811
     assert (p.kernel, p.tile_rows, p.waves, p.workgroups) == (0, 0, 0, 0)
     bad = attn(kv, q_heads=3)
     assert L.fp4_kv_attention_plan(q[0], q[1], ctypes.addressof(bad), ctypes.addressof(p)) == fp4.ERR_INVALID_ARG
+
+
+def test_more_tiles_than_are_counted_are_refused(kv):  # noqa: F811
+    """Tiles of 16 rows, one at least for each sequence and head, up to 2^30."""
+    from bit_gemm_fwht_amd import fp4
+    for seqs, heads, want in ((2 ** 20, 1024, fp4.OK), (2 ** 20 + 1, 1024, fp4.ERR_UNSUPPORTED),
+                              (2 ** 28, 4, fp4.OK), (2 ** 28, 5, fp4.ERR_UNSUPPORTED), (2 ** 28, 60000, fp4.ERR_UNSUPPORTED)):
+        args = cache(kv, kv_heads=heads), batch(kv, tokens=1, seqs=seqs), attn(kv, q_heads=heads), kv.PlanC()
+        assert kv.lib().fp4_kv_attention_plan(*(ctypes.addressof(x) for x in args)) == want
+
+
+@pytest.mark.parametrize("lens,heads,group", [([(1, 5000)], 8, 4), ([(1, 5000)], 65535, 1), ([(1, 9000)] * 3000, 64, 1),
+                                              ([(9, 5000)] * 20, 16, 2)])
+def test_wide_tables_are_still_split(kv, lens, heads, group):  # noqa: F811
+    """However many keys a table has room for, contexts are dealt in shares."""
+    for width in (40, 4000, 2 ** 20, 2 ** 23, 2 ** 24 - 32):
+        p = plan(kv, lens, heads, group, 16, 128, "bf16", max_context=0, table_pages=width, table_ld=width)
+        assert p.kernel in (kv.PLAN_ROWS_SPLIT, kv.PLAN_ROWS_NEAR), width
