@@ -931,7 +931,7 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
     const double tiles_us = step_us * steps_of(32 * nw) * (double)((ntiles + at_once - 1) / at_once);
     const double rows_us = 15.0 + 3.0 * steps_of(kRows) * (double)tiles / (4.0 * rows_waves(dtype, U) * cus);
     const int64_t slots = (int64_t)c.T * G / (32 * nw) + c.S;
-    if ((int64_t)c.T * G >= 2 * kRows * (int64_t)c.S && tiles_us < rows_us && slots * c.H < (int64_t(1) << 31)) {
+    if ((int64_t)c.T * G >= 2 * kRows * (int64_t)c.S && tiles_us < rows_us && slots * c.H <= kMaxGrid) {
         p.tile_slots = (int)slots;
         p.nw = nw;
         return p;
@@ -945,7 +945,7 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
         p.nw = 4 * waves;
         p.unit = kWholeTiles;
         p.share_min = 1;
-        p.grid = (int)std::min<int64_t>(std::min(tiles, most), 1 << 30);
+        p.grid = (int)std::min(std::min(tiles, most), kMaxGrid);
     } else {
         // Shares: four waves, so that a CU has a second workgroup to read for while one changes tiles or
         // joins its waves (64 sequences of 4127 tokens on average: 115 us, with one of eight 140 us).

@@ -1,6 +1,6 @@
 // The key / value cache: rows of K and V quantized into their pages as they are written, and read
-// back. One wave works for one block (page x kv head) of K or of V; grid: blocks that the batch may
-// touch, kv heads by four, K and V.
+// back. One wave works for one block (page x kv head) of K or of V; grid: pages that the batch may
+// touch (kMaxGrid at a time), kv heads by four, K and V (and again for the next kMaxGrid pages).
 //
 // A lane takes 4 channels of 16 tokens at a time: the rows' side is then read and written in pieces of 4
 // values a token next to one another across the lanes, K's pages in 4 bytes a token likewise, and V's
@@ -8,6 +8,8 @@
 // Nothing goes through LDS and no wave waits for another. Bound by memory: two prompts of 4096 tokens and
 // 32 heads (201 MB) are written in 48.7 us, 4.1 TB/s, 8 contexts (108 MB) read in 22.6 us, 4.8 TB/s, where
 // a large copy reaches 5.2; single tokens by the loads that hang on one another (sequence, page, row).
+#include <algorithm>
+
 #include "fp4_internal.h"
 #include "kv_device.h"
 
@@ -97,8 +99,8 @@ __global__ __launch_bounds__(kKvThreads) void k_kv_append(KvRowsArgs a) {
     const int lane = threadIdx.x & 63;
     const int h = blockIdx.y * (kKvThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (h >= c.H) return;
-    const bool is_v = blockIdx.z != 0;
-    const KvBlock b = kv_block(c, blockIdx.x);
+    const bool is_v = blockIdx.z & 1;
+    const KvBlock b = kv_block(c, (int)(blockIdx.x + (blockIdx.z >> 1) * gridDim.x));
     if (b.page < 0) return;
     const int D = c.D, P = c.P, quads = D >> 2;
     const int64_t blk = (int64_t)b.page * c.H + h;
@@ -228,8 +230,8 @@ __global__ __launch_bounds__(kKvThreads) void k_kv_read(KvRowsArgs a) {
     const int lane = threadIdx.x & 63;
     const int h = blockIdx.y * (kKvThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (h >= c.H) return;
-    const bool is_v = blockIdx.z != 0;
-    const KvBlock b = kv_block(c, blockIdx.x);
+    const bool is_v = blockIdx.z & 1;
+    const KvBlock b = kv_block(c, (int)(blockIdx.x + (blockIdx.z >> 1) * gridDim.x));
     if (b.page < 0) return;
     const int D = c.D, P = c.P, quads = D >> 2;
     const int64_t blk = (int64_t)b.page * c.H + h;
@@ -271,7 +273,9 @@ __global__ __launch_bounds__(kKvThreads) void k_kv_read(KvRowsArgs a) {
 }
 
 static dim3 kv_grid(const KvView& c) {
-    return dim3((unsigned)(c.T / c.P + 2 * c.S), (unsigned)((c.H + kKvThreads / 64 - 1) / (kKvThreads / 64)), 2);
+    const int64_t slots = c.T / c.P + 2 * (int64_t)c.S, rounds = (slots + kMaxGrid - 1) / kMaxGrid;
+    return dim3((unsigned)std::min(slots, kMaxGrid), (unsigned)((c.H + kKvThreads / 64 - 1) / (kKvThreads / 64)),
+                (unsigned)(2 * rounds));
 }
 
 hipError_t launch_kv_append(const KvRowsArgs& a, int dtype, hipStream_t s) {

@@ -11,6 +11,8 @@ namespace bgf {
 constexpr int kMaxKeys = 0x7FFFF000;
 // Tiles of 16 rows, and units of keys of them, in one call at most: their sums stay in 32 bits.
 constexpr int64_t kMaxUnits = int64_t(1) << 30;
+// Workgroups along one axis of a launch at most: its threads (512 each at most) have to stay below 2^32.
+constexpr int64_t kMaxGrid = int64_t(1) << 22;
 
 // Cache and batch of one call (layouts in include/fp4.h).
 struct KvView {

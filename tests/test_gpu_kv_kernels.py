@@ -361,3 +361,22 @@ def test_a_tile_gives_the_same_bits_whatever_else_is_in_the_batch():
         p = kv.attention_plan(s.cache, b, n, 128)
         assert (p.kernel, p.tile_rows) == (TILES, 256)
     assert torch.equal(kv.attention(q[576:], s.cache, one), kv.attention(q, s.cache, s.batch)[576:])
+
+
+# ------------------------------------------------------------------------------------- long batches
+def test_batches_of_more_pages_than_one_axis_of_a_launch_takes():
+    """2^28 + 37 tokens of one head in pages of 16, more than 2^24 of them: written and read back, whole
+    numbers that E4M3 holds exactly under any scale of theirs."""
+    page, dim = 16, 16
+    tokens = 2 ** 28 + 37
+    pages = -(-tokens // page)
+    g = torch.Generator(device=DEV).manual_seed(49)
+    rows = torch.randint(-8, 9, (2, tokens, 1, dim), generator=g, device=DEV, dtype=torch.int8)
+    k, v = rows[0].to(torch.bfloat16), rows[1].to(torch.bfloat16)
+    cache = kv.empty_cache(pages, 1, page, dim, DEV)
+    table = torch.arange(pages - 1, -1, -1, device=DEV, dtype=torch.int32)[None]
+    batch = kv.Batch(torch.tensor([0, tokens], dtype=torch.int32, device=DEV),
+                     torch.tensor([tokens], dtype=torch.int32, device=DEV), table)
+    kv.append(cache, k, v, batch)
+    for got, want in zip(kv.read(cache, batch, tokens), (k, v)):
+        assert torch.equal(got, want)

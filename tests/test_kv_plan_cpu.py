@@ -74,3 +74,16 @@ def test_wide_tables_are_still_split(kv, lens, heads, group):  # noqa: F811
     for width in (40, 4000, 2 ** 20, 2 ** 23, 2 ** 24 - 32):
         p = plan(kv, lens, heads, group, 16, 128, "bf16", max_context=0, table_pages=width, table_ld=width)
         assert p.kernel in (kv.PLAN_ROWS_SPLIT, kv.PLAN_ROWS_NEAR), width
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [16, 128, 256])
+@pytest.mark.parametrize("tokens,seqs,heads,group", [
+    (2 ** 22, 2 ** 22, 32, 1), (2 ** 22, 2 ** 18, 32, 1), (2 ** 26, 1, 32, 1), (2 ** 27, 1, 32, 2), (2 ** 29, 1, 16, 1),
+    (2 ** 24, 1, 1, 64), (2 ** 27, 2 ** 20, 4, 8),
+])
+def test_launches_stay_within_2_32_threads(kv, tokens, seqs, heads, group, dim, dtype):  # noqa: F811
+    for context, window in ((64, 0), (2000, 0), (2 ** 20, 0), (2 ** 20, 16)):
+        p = plan(kv, [(1, context)], heads, group, dim, 128, dtype, window, tokens=tokens, seqs=seqs,
+                 max_tokens=-(-tokens // seqs), max_context=context)
+        assert 0 < p.workgroups * p.waves * 64 < 2 ** 32
