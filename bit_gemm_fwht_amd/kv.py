@@ -136,9 +136,22 @@ class Batch:
         self.device = table.device
         fp4._on(self.device, cu_tokens, context)
         self.cu_tokens, self.context, self.table, self.seqs = cu_tokens, context, table, seqs
-        self._c = BatchC(cu_tokens.data_ptr(), context.data_ptr(), table.data_ptr(), 0,
-                         table.stride(0) if seqs > 1 else width, seqs, width, max_tokens or 0, max_context or 0)
-        self._p = ctypes.addressof(self._c)
+        self._last = self._make(0, cu_tokens.data_ptr(), context.data_ptr(), table.data_ptr(),
+                                table.stride(0) if seqs > 1 else width, max_tokens or 0, max_context or 0)
+
+    def _make(self, tokens, cu_tokens, context, table, table_ld, max_tokens, max_context):
+        c = BatchC(cu_tokens, context, table, tokens, table_ld, self.seqs, self.table.shape[1], max_tokens, max_context)
+        return tokens, ctypes.addressof(c), c
+
+    def _at(self, tokens: int):
+        """(tokens, address, struct) for calls of so many rows, never changed once made: threads may use
+        one batch with different row counts. The last one is kept."""
+        last = self._last
+        if last[0] != tokens:
+            c = last[2]
+            last = self._last = self._make(tokens, c.cu_tokens, c.context, c.table, c.table_ld, c.max_tokens,
+                                           c.max_context)
+        return last
 
 
 def _rows(t: torch.Tensor, heads, dim: int, dev, name: str) -> int:
@@ -156,10 +169,10 @@ def _rows(t: torch.Tensor, heads, dim: int, dev, name: str) -> int:
     return code
 
 
-def _use(cache: KVCache, batch: Batch, tokens: int) -> None:
+def _use(cache: KVCache, batch: Batch, tokens: int):
     if batch.device != cache.device:
         raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
-    batch._c.tokens = tokens
+    return batch._at(tokens)
 
 
 def _stream(dev: torch.device) -> int:
@@ -180,8 +193,8 @@ def append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, batch: Batch, scale
     code = _rows(k, cache.kv_heads, cache.head_dim, dev, "k")
     if _rows(v, cache.kv_heads, cache.head_dim, dev, "v") != code or v.shape[0] != k.shape[0]:
         raise ValueError("k and v must have one dtype and one number of tokens")
-    _use(cache, batch, k.shape[0])
-    st = lib().fp4_kv_append(cache._p, batch._p, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+    b = _use(cache, batch, k.shape[0])
+    st = lib().fp4_kv_append(cache._p, b[1], k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
                              v.stride(1), code, scale_mode, _stream(dev))
     _check(st, "fp4_kv_append")
 
@@ -198,8 +211,8 @@ def read(cache: KVCache, batch: Batch, tokens: int, dtype=torch.bfloat16, out=No
     code = _rows(k, cache.kv_heads, cache.head_dim, dev, "k")
     if _rows(v, cache.kv_heads, cache.head_dim, dev, "v") != code or k.shape[0] != tokens or v.shape[0] != tokens:
         raise ValueError(f"out must be two tensors of one dtype with {tokens} tokens")
-    _use(cache, batch, tokens)
-    st = lib().fp4_kv_read(cache._p, batch._p, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+    b = _use(cache, batch, tokens)
+    st = lib().fp4_kv_read(cache._p, b[1], k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
                            v.stride(1), code, _stream(dev))
     _check(st, "fp4_kv_read")
     return k, v
@@ -208,9 +221,9 @@ def read(cache: KVCache, batch: Batch, tokens: int, dtype=torch.bfloat16, out=No
 def attention_workspace_bytes(cache: KVCache, batch: Batch, tokens: int, q_heads: int, dtype=torch.bfloat16,
                               window: int = 0) -> int:
     """Bytes of workspace attention() needs for q [tokens, q_heads, head_dim]."""
-    _use(cache, batch, tokens)
+    b = _use(cache, batch, tokens)
     a = AttnC(None, None, None, 0, 0, 0, 0, _CODES[dtype], q_heads, 1, min(window, _NO_WINDOW), 1.0)
-    n = lib().fp4_kv_attention_workspace_bytes(cache._p, batch._p, ctypes.addressof(a))
+    n = lib().fp4_kv_attention_workspace_bytes(cache._p, b[1], ctypes.addressof(a))
     if n < 0:
         raise Fp4Error(fp4.ERR_INVALID_ARG, "fp4_kv_attention_workspace_bytes")
     return n
@@ -220,10 +233,10 @@ def attention_plan(cache: KVCache, batch: Batch, tokens: int, q_heads: int, dtyp
                    window: int = 0) -> PlanC:
     """How attention() of q [tokens, q_heads, head_dim] would be carried out: kernel (PLAN_...), tile_rows,
     waves, workgroups."""
-    _use(cache, batch, tokens)
+    b = _use(cache, batch, tokens)
     a = AttnC(None, None, None, 0, 0, 0, 0, _CODES[dtype], q_heads, 1, min(window, _NO_WINDOW), 1.0)
     p = PlanC()
-    _check(lib().fp4_kv_attention_plan(cache._p, batch._p, ctypes.addressof(a), ctypes.addressof(p)),
+    _check(lib().fp4_kv_attention_plan(cache._p, b[1], ctypes.addressof(a), ctypes.addressof(p)),
            "fp4_kv_attention_plan")
     return p
 
@@ -246,13 +259,13 @@ def attention(q: torch.Tensor, cache: KVCache, batch: Batch, scale: float | None
     if lse is not None:
         _device_tensor(lse, torch.float32, (tokens, heads), "lse")
         fp4._on(dev, lse)
-    _use(cache, batch, tokens)
+    b = _use(cache, batch, tokens)
     a = AttnC(q.data_ptr(), out.data_ptr(), lse.data_ptr() if lse is not None else None, q.stride(0), q.stride(1),
               out.stride(0), out.stride(1), code, heads, causal, min(window, _NO_WINDOW),
               scale if scale is not None else 1.0 / math.sqrt(dim))
     pa = ctypes.addressof(a)
     L = lib()
-    need = L.fp4_kv_attention_workspace_bytes(cache._p, batch._p, pa)
+    need = L.fp4_kv_attention_workspace_bytes(cache._p, b[1], pa)
     ws = None
     if need > 0:
         if workspace is None:
@@ -260,7 +273,7 @@ def attention(q: torch.Tensor, cache: KVCache, batch: Batch, scale: float | None
         else:
             fp4._ws_bytes(workspace, need, dev)
         ws = workspace.data_ptr()
-    st = L.fp4_kv_attention(cache._p, batch._p, pa, ws, need, _stream(dev))
+    st = L.fp4_kv_attention(cache._p, b[1], pa, ws, need, _stream(dev))
     _check(st, "fp4_kv_attention")
     return out
 

@@ -380,3 +380,26 @@ def test_batches_of_more_pages_than_one_axis_of_a_launch_takes():
     kv.append(cache, k, v, batch)
     for got, want in zip(kv.read(cache, batch, tokens), (k, v)):
         assert torch.equal(got, want)
+
+
+# --------------------------------------------------------------------------- one batch, many threads
+def test_calls_of_different_row_counts_share_a_batch(monkeypatch):
+    """A call with other rows that comes between the size query and the call of a first one (as another
+    thread's may: the library's calls run without the interpreter's lock) takes nothing from it."""
+    s = Setup([(4, 5000), (3, 4000)], 2, 64, 32, seed=50)
+    q = s.draw(8, "bf16")
+    want = kv.attention(q, s.cache, s.batch).clone()
+    first = kv.attention(q[:4], s.cache, s.batch).clone()
+    real, between = kv.lib().fp4_kv_attention_workspace_bytes, []
+
+    def query(*args):
+        n = real(*args)
+        if not between:
+            between.append(None)
+            between.append(kv.attention(q[:4], s.cache, s.batch))
+        return n
+
+    monkeypatch.setattr(kv.lib(), "fp4_kv_attention_workspace_bytes", query)
+    out = torch.full_like(q, math.nan)
+    kv.attention(q, s.cache, s.batch, out=out)
+    assert torch.equal(out, want) and torch.equal(between[1], first)
