@@ -148,7 +148,7 @@ __device__ __forceinline__ int units_from(const KvAttnArgs& a, int p0, int keys)
     return a.window ? min(max(window_from(p0, a.window), 0), keys) & ~63 : 0;
 }
 
-// tiles of a sequence, units of each of them, and its units in all
+// tiles of a sequence, units of each of them, and its units in all (-1: cu_tokens descends)
 __device__ __forceinline__ int seq_units(const KvAttnArgs& a, int s, int* tiles, int* units) {
     const KvView& c = a.c;
     const int n = cu_at(c, s + 1) - cu_at(c, s), ctx = max(c.ctx[s], 0);
@@ -156,7 +156,7 @@ __device__ __forceinline__ int seq_units(const KvAttnArgs& a, int s, int* tiles,
     const int lo = units_from(a, ctx - n, keys);
     *tiles = max(n * a.G + kRows - 1, 0) / kRows;
     *units = keys > lo ? (int)(((uint32_t)(keys - lo) + a.unit - 1) / a.unit) : 1;
-    return c.H * *tiles * *units;
+    return n < 0 ? -1 : c.H * *tiles * *units;
 }
 
 // The batch's units, and the place of one of them. All lanes of a wave take part; lane i counts
@@ -179,10 +179,14 @@ __device__ __forceinline__ void count_64(const KvAttnArgs& a, int s0, Units* q) 
 __device__ __forceinline__ Units count_units(const KvAttnArgs& a) {
     Units q;
     q.total = 0;
+    uint64_t down = 0;
     for (int s0 = 0; s0 < a.c.S; s0 += 64) {
         count_64(a, s0, &q);
         q.total += __builtin_amdgcn_readlane(q.upto, 63);
+        down |= __ballot(q.count < 0);
     }
+    // (the host holds the sum to kMaxUnits for rows that are counted once: a batch that descends has more)
+    if (down) q.total = 0;
     q.share = max((int)(((unsigned)q.total + a.grid - 1) / (unsigned)a.grid), a.share_min);
     return q;
 }

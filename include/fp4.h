@@ -298,7 +298,8 @@ int fp4_nvfp4_to_mxfp8(const void* codes, const void* scales, int64_t rows, int6
  *
  * A batch says how the rows of q, k and v belong to sequences and where those live (device int32):
  *   cu_tokens [seqs + 1]   rows cu_tokens[s] .. cu_tokens[s + 1] - 1 are sequence s's (a sequence may
- *                          have none); ascending from 0 to tokens
+ *                          have none); ascending from 0 to tokens (in a batch that descends rows hold
+ *                          anything, and nothing outside them is touched)
  *   context   [seqs]       the sequence's tokens in the cache, the batch's own included: row i of a
  *                          sequence with n rows is its token context - n + i (no token if negative)
  *   table     [seqs, table_pages], row pitch table_ld: the sequence's pages in order; token t is in

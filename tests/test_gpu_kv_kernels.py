@@ -403,3 +403,24 @@ def test_calls_of_different_row_counts_share_a_batch(monkeypatch):
     out = torch.full_like(q, math.nan)
     kv.attention(q, s.cache, s.batch, out=out)
     assert torch.equal(out, want) and torch.equal(between[1], first)
+
+
+# -------------------------------------------------------------------------- batches that descend
+@pytest.mark.parametrize("name", ["rows, 70 sequences", "split, 80", "near, 128", "eight waves, uneven", "four waves, 80"])
+def test_batches_that_descend_touch_their_rows_only(name):
+    """cu_tokens out of order and out of range: every call returns and stays inside the rows it was given,
+    and the next call with a sound batch is right."""
+    s, q_heads, dtype, hs = setup(name, seed=51)
+    good = s.batch.cu_tokens.clone()
+    g = torch.Generator(device=DEV).manual_seed(51)
+    cu = good[torch.randperm(len(good), generator=g, device=DEV)]
+    cu[0], cu[-1] = 2 ** 31 - 1, -5
+    s.batch.cu_tokens.copy_(cu)
+    room = torch.full((s.tokens + 20, q_heads, s.dim), 9.0, device=DEV, dtype=DT[dtype])
+    kv.attention(s.draw(q_heads, dtype), s.cache, s.batch, out=room[10:-10])
+    spaces = [torch.full((s.tokens + 20, s.heads, s.dim), 9.0, device=DEV, dtype=DT[dtype]) for _ in range(2)]
+    kv.read(s.cache, s.batch, s.tokens, out=tuple(x[10:-10] for x in spaces))
+    for x in (room, *spaces):
+        assert (x[:10] == 9.0).all() and (x[-10:] == 9.0).all()
+    s.batch.cu_tokens.copy_(good)
+    check(s, q_heads, dtype, kv_heads=hs)
