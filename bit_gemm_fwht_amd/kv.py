@@ -154,11 +154,16 @@ class Batch:
         return last
 
 
+def _code(dtype, name: str) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {dtype}: float32 or bfloat16")
+    return code
+
+
 def _rows(t: torch.Tensor, heads, dim: int, dev, name: str) -> int:
     """Check [tokens, heads, dim] rows of bf16 / fp32 on dev; returns the dtype code."""
-    code = _CODES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}: float32 or bfloat16")
+    code = _code(t.dtype, name)
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
     shape = t.shape
@@ -222,7 +227,7 @@ def attention_workspace_bytes(cache: KVCache, batch: Batch, tokens: int, q_heads
                               window: int = 0) -> int:
     """Bytes of workspace attention() needs for q [tokens, q_heads, head_dim]."""
     b = _use(cache, batch, tokens)
-    a = AttnC(None, None, None, 0, 0, 0, 0, _CODES[dtype], q_heads, 1, min(window, _NO_WINDOW), 1.0)
+    a = AttnC(None, None, None, 0, 0, 0, 0, _code(dtype, "q"), q_heads, 1, min(window, _NO_WINDOW), 1.0)
     n = lib().fp4_kv_attention_workspace_bytes(cache._p, b[1], ctypes.addressof(a))
     if n < 0:
         raise Fp4Error(fp4.ERR_INVALID_ARG, "fp4_kv_attention_workspace_bytes")
@@ -234,7 +239,7 @@ def attention_plan(cache: KVCache, batch: Batch, tokens: int, q_heads: int, dtyp
     """How attention() of q [tokens, q_heads, head_dim] would be carried out: kernel (PLAN_...), tile_rows,
     waves, workgroups."""
     b = _use(cache, batch, tokens)
-    a = AttnC(None, None, None, 0, 0, 0, 0, _CODES[dtype], q_heads, 1, min(window, _NO_WINDOW), 1.0)
+    a = AttnC(None, None, None, 0, 0, 0, 0, _code(dtype, "q"), q_heads, 1, min(window, _NO_WINDOW), 1.0)
     p = PlanC()
     _check(lib().fp4_kv_attention_plan(cache._p, b[1], ctypes.addressof(a), ctypes.addressof(p)),
            "fp4_kv_attention_plan")

@@ -8,6 +8,7 @@ import torch
 
 import kv_reference as ref
 from bit_gemm_fwht_amd import kv
+from bit_gemm_fwht_amd.fp4 import Fp4Error
 from test_gpu_kv import DEV, DT, Setup, host
 
 pytestmark = pytest.mark.gpu
@@ -424,3 +425,12 @@ def test_batches_that_descend_touch_their_rows_only(name):
         assert (x[:10] == 9.0).all() and (x[-10:] == 9.0).all()
     s.batch.cu_tokens.copy_(good)
     check(s, q_heads, dtype, kv_heads=hs)
+
+
+def test_queries_refuse_types_as_the_calls_do():
+    s = Setup([(2, 20)], 2, 64, 16)
+    for ask in (kv.attention_workspace_bytes, kv.attention_plan):
+        with pytest.raises(TypeError):
+            ask(s.cache, s.batch, 2, 4, torch.float16)
+        with pytest.raises(Fp4Error):
+            ask(s.cache, s.batch, 2, 3)
