@@ -35,9 +35,11 @@ __device__ __forceinline__ bf16x8 cvt8(uint32_t a, uint32_t b, float scale) {
     return __builtin_bit_cast(bf16x8, r);
 }
 
-// 8 floats as sums of NS bf16. NS = 1: rounded. NS = 2: cut after 8 significant bits, the rest rounded:
-// 2^-17 off at most, which keeps softmax weights (rounded to one bf16 they would add as much error as
-// the bf16 output's own rounding) out of the result for one more product. NS = 3: exact (the 24
+// 8 floats as sums of NS bf16. NS = 1: rounded. NS = 2: cut after 8 significant bits, the rest (below 2^-7 of
+// the value's power of two) rounded to 8: 2^-16 off at most, which keeps softmax weights (rounded to one
+// bf16 they would add as much error as the bf16 output's own rounding) out of the result for one more
+// product; with a third the error against 64 bits stays the same to five digits (prompt of 4096 tokens
+// 1.6112e-3, windowed chunks 1.6417e-3, the output's rounding). NS = 3: exact (the 24
 // significant bits in three runs of 8), so that products with bf16 lose nothing of an fp32 operand.
 // INF: the values may be infinite (queries); an infinity has no rest (inf - inf would be NaN).
 template <int NS, bool INF>
@@ -133,8 +135,8 @@ __device__ __forceinline__ void store_out4(void* out, int64_t at, f32x4 y) {
 // What there is to do is counted in units of a.unit keys of a tile of a kv head (2^31: of whole tiles),
 // sequence by sequence; every workgroup takes the same number of consecutive units (a.share_min at least), wherever in a tile
 // they begin and end. However uneven the contexts, all CUs read as much: a step of 64 sequences of 4127
-// tokens on average (32 heads on 8 kv heads, 554 MB) takes 115 + 7 us, 4.8 TB/s, two of 131071 tokens 97 + 8
-// us, 5.5 TB/s of the 5.96 that plain reading reaches; bound by the reads and, where tiles change within a
+// tokens on average (32 heads on 8 kv heads, 554 MB) takes 113 + 9 us, 4.9 TB/s, two of 131071 tokens 98 + 9
+// us, 5.4 TB/s of the 5.96 that plain reading reaches; bound by the reads and, where tiles change within a
 // share, by the latency of the next one's first keys. A tile that lies
 // within one workgroup's share is written as output. Of the others each workgroup leaves at most two
 // partial results, of the tile that its share begins in (place 0) and of the one that it ends in
@@ -564,7 +566,9 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs a) {
 // taken, the second operand of O^T's product: 16 consecutive keys in a lane. Weights enter as sums of two
 // bf16 (fp32 queries: three), cut and rounded next to the products, where the vector unit has time.
 // A prompt of 4096 tokens and 32 heads of 128 takes 203 us, 680 TFLOP/s of attention (1020 of products),
-// bound by the vector instructions of the softmax: beside a wave that multiplies, each takes 7 to 12 clk.
+// bound by the vector instructions of the softmax: a wave's step has 48 products (1536 clk) and over 300
+// vector instructions, which beside a wave that multiplies take 7 to 12 clk each, so that a half step lasts
+// 3400 clk and the matrix cores are busy 45 % of the time that CUs work.
 // (Weights as one fp16 each take 160 us instead of 206 for a prompt of 4096 tokens and 32 heads, but lose channels to which
 // only keys of small weight contribute: fp16 ends 2^-24 below 1.)
 // ---------------------------------------------------------------------------------------------
@@ -917,13 +921,17 @@ KvAttnPlan plan_kv_attention(const KvView& c, int Hq, int window, int dtype, int
     };
     const int64_t tiles = tiles_of(kRows);
 
-    // Which kernel: by the time of their steps of 64 keys, as measured. In rows of 16 a wave's step takes
-    // 3 us (2.3 to 3.8), with 4 or 8 waves on a CU at a time whatever the number of tiles, and splitting and
-    // joining take about 15 us; in tiles a workgroup goes through all of its tile's keys: a step of four
-    // waves takes 2.1 us alone on a CU, 2.7 us with a second workgroup there, one of eight waves 3.0 us, and
-    // more where a lane holds more. (4096 tokens of 32 heads: 203 us in tiles, 390 us in rows; 512 rows of
-    // one head over 32000 keys: 1.1 ms in tiles, 52 us in rows.) Tiles are of 128 rows unless there are
-    // more of them than two for a CU.
+    // Which kernel: by the time of their steps of 64 keys, as measured, every tile taken to go through all
+    // keys. In rows of 16 a wave's step takes 3 us (2.5 us where tiles of a head meet in L2, 5 to 7 us where
+    // every step comes from memory, as only few rows do), with 4 or 8 waves on a CU at a time whatever the
+    // number of tiles, and splitting and joining take about 15 us; in tiles a workgroup goes through all of
+    // its tile's keys: a step of four waves takes 2.1 us alone on a CU, 2.7 us with a second workgroup there,
+    // one of eight waves 3.0 us, and more where a lane holds more. (4096 tokens of 32 heads: 203 us in
+    // tiles, 639 us in rows; 500 over 500 tokens of 32 heads on 8: 23 and 44 us; 512 rows of one head over
+    // 32000 keys: 1.0 ms in tiles, 52 us in rows; 512 rows of 32 heads over 4096 keys: 134 and 96 us; wrong
+    // for prompts of fp32 heads of 256, whose causal tiles have half the steps: 2048 tokens of 32 heads go
+    // to rows, 422 us, and would take 270 us in tiles.) Tiles are of 128 rows unless there are more of them
+    // than two for a CU.
     const bool wide = tile_nw(dtype, U) == 8;  // the variants of which two workgroups fit a CU
     const int nw = wide && tiles_of(128) > 2 * cus ? 8 : 4;
     const auto steps_of = [&](int r) {

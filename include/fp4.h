@@ -362,7 +362,9 @@ int fp4_kv_read(const fp4_kv_cache* cache, const fp4_kv_batch* batch, void* k, i
  * that are not allowed for any query of a sequence (past its context, pages before every window)
  * is never used, whatever its bits. Scores, softmax statistics and sums are fp32; with fp32 q, q and
  * the weights enter the matrix products as exact sums of three bf16, with bf16 q the weights as sums
- * of two (2^-17 off at most; K and V enter exactly). Results do not depend on timing: no atomics.
+ * of two (2^-16 off at most; K and V enter exactly). Results do not depend on timing: no atomics. Scores
+ * that leave fp32's range on the way are outside the contract (|q| past 2^100, a scale below 2^-100 that is
+ * not 0).
  * lse: fp32 [tokens, q_heads], contiguous, or NULL. workspace: at least
  * fp4_kv_attention_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0; -1 for arguments
  * that the call would reject); it holds the partial results of keys split over the chip. */
@@ -378,6 +380,7 @@ typedef struct fp4_kv_attn {
     int32_t window;
     float scale;
 } fp4_kv_attn;
+
 /* How the call would be carried out, for profiles and tests: which kernel, the rows of a tile, the waves of a
  * workgroup, the workgroups of the main launch. A choice of speed alone, free to change. tokens == 0:
  * all zero. */

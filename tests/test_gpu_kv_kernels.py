@@ -381,6 +381,8 @@ def test_batches_of_more_pages_than_one_axis_of_a_launch_takes():
     kv.append(cache, k, v, batch)
     for got, want in zip(kv.read(cache, batch, tokens), (k, v)):
         assert torch.equal(got, want)
+    del rows, k, v, cache, got, want
+    torch.cuda.empty_cache()
 
 
 # --------------------------------------------------------------------------- one batch, many threads
