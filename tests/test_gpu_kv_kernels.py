@@ -210,6 +210,8 @@ KERNELS = {
     "rows, 70 sequences": (ragged(70, 1, 1000), 2, 4, 128, 32, "bf16", ROWS, 16),
     "rows, 150 sequences": (ragged(150, 3, 700), 1, 5, 80, 16, "bf16", ROWS, 16),
     "rows, 129 sequences, fp32": (ragged(129, 2, 500), 1, 3, 256, 64, "f32", ROWS, 16),
+    "rows, 5000 sequences": (ragged(5000, 2, 60), 1, 2, 32, 16, "bf16", ROWS, 16),
+    "split, 300 sequences": (ragged(300, 2, 3000), 1, 2, 32, 16, "f32", SPLIT, 16),
     "split, 100 sequences": (ragged(100, 1, 5000), 2, 4, 64, 32, "bf16", SPLIT, 16),
     "split, 80": (ragged(5, 2, 7000), 2, 3, 80, 16, "bf16", SPLIT, 16),
     "split, 256": (ragged(3, 1, 6000), 2, 8, 256, 128, "bf16", SPLIT, 16),
@@ -225,6 +227,7 @@ KERNELS = {
     "eight waves, 112": ([(600, 600)], 32, 4, 112, 16, "bf16", TILES, 256),
     "eight waves, 64, fp32": (UNEVEN, 16, 4, 64, 32, "f32", TILES, 256),
     "eight waves, 32, fp32": ([(600, 700)], 32, 4, 32, 32, "f32", TILES, 256),
+    "eight waves, 300 sequences": ([(20 + i % 41, 70 + i % 97) for i in range(300)], 2, 8, 32, 16, "bf16", TILES, 256),
     "four waves, 128": ([(700, 1500), (33, 40)], 8, 4, 128, 32, "bf16", TILES, 128),
     "four waves, 80": ([(400, 900)], 4, 8, 80, 16, "bf16", TILES, 128),
     "four waves, 192": ([(232, 440)], 16, 8, 192, 64, "bf16", TILES, 128),
@@ -436,3 +439,18 @@ def test_queries_refuse_types_as_the_calls_do():
             ask(s.cache, s.batch, 2, 4, torch.float16)
         with pytest.raises(Fp4Error):
             ask(s.cache, s.batch, 2, 3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_thousands_of_sequences_are_written_and_read(dtype):
+    """More sequences than two steps of a search by 64 tell apart, every seventh without a row."""
+    lens = [(i * 5 % 7, i * 5 % 7 + i % 40) for i in range(5000)]
+    s = Setup(lens, 2, 16, 16, seed=52)
+    k, v = s.draw(2, dtype), s.draw(2, dtype)
+    ref.append(s.ref, host(k), host(v), s.cu, s.context, s.table, True)
+    kv.append(s.cache, k, v, s.batch)
+    for got, want in ((s.cache.k_scales, s.ref.ks), (s.cache.v_scales, s.ref.vs), (s.cache.k_codes, s.ref.k),
+                      (s.cache.v_codes, s.ref.v)):
+        assert np.array_equal(got.cpu().numpy(), want)
+    for got, want in zip(kv.read(s.cache, s.batch, s.tokens), ref.read(s.ref, s.cu, s.context, s.table)):
+        assert np.array_equal(host(got), rounded(want, "bf16"))
