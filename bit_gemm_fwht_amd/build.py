@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbgf.so")
 SOURCES = ["fp4_abi.cpp", "quantize.hip", "gemm.hip", "transpose.hip", "kv_abi.cpp", "kv_cache.hip",
-           "kv_attention.hip"]
+           "kv_attention.hip", "layer_abi.cpp", "norm.hip", "rope.hip", "gated.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -104,6 +104,13 @@ struct GemmArgs {
     uint8_t* sa8;
     uint8_t* b8;
     uint8_t* sb8;
+    // gated feed-forward: b / sb are the gate's, N = F; the up projection and what it writes beside c = h
+    const uint8_t* b_up;
+    const uint8_t* sb_up;
+    void* gu;                // [M, 2 N], or NULL
+    int64_t ldgu;
+    float* h32;              // [M, N] fp32 for a quantize pass of its own, or NULL
+    int act;
 };
 
 // NVFP4 [rows, cols] -> E4M3 [rows, cols] + E8M0 [rows, cols / 32] (the GEMM's FP8 re-expression)

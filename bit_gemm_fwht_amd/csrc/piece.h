@@ -1,0 +1,186 @@
+// Rows in pieces of 8 consecutive elements, one piece a lane and consecutive pieces in consecutive lanes:
+// loads and stores of a wave are whole runs of memory, no transposition is needed, and a stochastic rounding's
+// random words are one call a piece. An MX group of 32 is four lanes, a rotated chunk of n elements n / 8.
+// The rotation's stages h = 1, 2, 4 run in registers, h = 8 .. 128 pair lane l with l ^ 1 .. l ^ 16, in the
+// order and with the roundings of fwht_segment, so that the codes are the same as fp4_quantize's.
+#pragma once
+
+#include "device.h"
+#include "layer_internal.h"
+#include "quant_block.h"
+
+namespace bgf {
+
+// raw words of a piece: 16 bytes of bf16, 32 of fp32
+template <int DT>
+struct Piece {
+    static constexpr int N = DT == DT_BF16 ? 1 : 2;
+    u32x4 w[N];
+};
+
+template <int DT>
+__device__ __forceinline__ void piece_load(Piece<DT>& p, const void* base, int64_t elem) {
+    const u32x4* s = reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base) + elem * (DT == DT_BF16 ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < Piece<DT>::N; ++i) p.w[i] = s[i];
+}
+
+template <int DT>
+__device__ __forceinline__ void piece_zero(Piece<DT>& p) {
+#pragma unroll
+    for (int i = 0; i < Piece<DT>::N; ++i) p.w[i] = (u32x4){0u, 0u, 0u, 0u};
+}
+
+template <int DT>
+__device__ __forceinline__ void piece_values(const Piece<DT>& p, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (DT == DT_BF16) v[j] = (j & 1) ? bf16_hi(p.w[0][j >> 1]) : bf16_lo(p.w[0][j >> 1]);
+        else v[j] = __uint_as_float(p.w[j >> 2][j & 3]);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ Piece<DT> piece_pack(const float (&v)[8]) {
+    Piece<DT> p;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        if constexpr (DT == DT_BF16) {
+            p.w[0][j >> 1] = pack_bf16x2_rne(v[j], v[j + 1]);
+        } else {
+            p.w[j >> 2][j & 3] = __float_as_uint(v[j]);
+            p.w[j >> 2][(j & 3) + 1] = __float_as_uint(v[j + 1]);
+        }
+    }
+    return p;
+}
+
+template <int DT>
+__device__ __forceinline__ void piece_store(void* base, int64_t elem, const Piece<DT>& p) {
+    u32x4* d = reinterpret_cast<u32x4*>(reinterpret_cast<char*>(base) + elem * (DT == DT_BF16 ? 2 : 4));
+#pragma unroll
+    for (int i = 0; i < Piece<DT>::N; ++i) d[i] = p.w[i];
+}
+
+// One stage of the rotation between lanes l and l ^ M: a + b in the lower lane, a - b in the upper.
+template <int M>
+__device__ __forceinline__ void fwht_lanes(float (&v)[8]) {
+    const float sgn = (__lane_id() & M) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], sgn, lane_xor<M>(v[i]));
+}
+
+// Blockwise H_n / sqrt(n), n in {0, 16, .., 256} the same for the whole wave, every lane taking part.
+__device__ __forceinline__ void fwht_piece(float (&v)[8], int n) {
+    if (n == 0) return;
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & h)) {
+                const float a = v[i], b = v[i + h];
+                v[i] = a + b;
+                v[i + h] = a - b;
+            }
+    fwht_lanes<1>(v);
+    if (n >= 32) fwht_lanes<2>(v);
+    if (n >= 64) fwht_lanes<4>(v);
+    if (n >= 128) fwht_lanes<8>(v);
+    if (n >= 256) fwht_lanes<16>(v);
+    const float c = n == 16 ? inv_sqrt_n<16>() : n == 32 ? inv_sqrt_n<32>() : n == 64 ? inv_sqrt_n<64>()
+                  : n == 128 ? inv_sqrt_n<128>() : inv_sqrt_n<256>();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * c;
+}
+
+// Codes of a piece under the block exponent k: 4 bytes of E2M1 in out[0], 8 of E4M3 in out[0], out[1].
+template <int ELEM, int RND>
+__device__ __forceinline__ void piece_encode(float (&v)[8], int k, uint64_t seed, uint64_t idx, uint32_t (&out)[2]) {
+    if (k == -127) {  // 2^-127 is not a normal fp32: 2^-126 after doubling (exact for such tiny values)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * 2.0f;
+        k = -126;
+    }
+    const float scale = pow2f(k);
+    if constexpr (RND == RND_RNE) {
+        if constexpr (ELEM == ELEM_E2M1) {
+            uint32_t r = cvt_fp4x2<0>(0u, v[0], v[1], scale);
+            r = cvt_fp4x2<1>(r, v[2], v[3], scale);
+            r = cvt_fp4x2<2>(r, v[4], v[5], scale);
+            out[0] = cvt_fp4x2<3>(r, v[6], v[7], scale);
+        } else {
+            const float top = 448.0f * scale;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_fmed3f(v[i], -top, top);
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const uint32_t r = cvt_fp8x2<false>(0u, v[4 * w], v[4 * w + 1], scale);
+                out[w] = cvt_fp8x2<true>(r, v[4 * w + 2], v[4 * w + 3], scale);
+            }
+        }
+    } else {
+        const float rcp = __builtin_amdgcn_ldexpf(1.0f, -k);
+        uint32_t c[4];
+        philox_group(SrSource{seed, idx}, 0, c);
+        out[0] = out[1] = 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (ELEM == ELEM_E2M1) out[0] |= e2m1_sr(v[j] * rcp, sr_u16(c, j)) << (4 * j);
+            else out[j >> 2] |= e4m3_sr(v[j] * rcp, sr_u16(c, j)) << (8 * (j & 3));
+        }
+    }
+}
+
+// Rotate, scale and encode the wave's pieces and store those that are `valid`. idx: the piece's first
+// element in the row-major output (a multiple of 8; pieces of a group in four lanes 4 i .. 4 i + 3).
+template <int RND>
+__device__ __forceinline__ void piece_quantize(const QuantOut& q, float (&v)[8], int64_t idx, bool valid) {
+    fwht_piece(v, q.hn);
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    m = fmaxf(m, lane_xor<1>(m));
+    m = fmaxf(m, lane_xor<2>(m));
+    uint32_t out[2];
+    int k;
+    if (q.elem == ELEM_E2M1) {
+        k = e8m0_exp<2, 0x400000u>(m, q.ceil_rule != 0);
+        piece_encode<ELEM_E2M1, RND>(v, k, q.seed, (uint64_t)idx, out);
+        if (valid) *reinterpret_cast<uint32_t*>(q.codes + (idx >> 1)) = out[0];
+    } else {
+        k = e8m0_exp<8, 0x600000u>(m, q.ceil_rule != 0);
+        piece_encode<ELEM_E4M3, RND>(v, k, q.seed, (uint64_t)idx, out);
+        if (valid) *reinterpret_cast<u32x2*>(q.codes + idx) = (u32x2){out[0], out[1]};
+    }
+    if (valid && !(__lane_id() & 3)) q.scales[idx >> 5] = (uint8_t)(k + 127);
+}
+
+// The activation of a gated feed-forward and its derivative.
+constexpr float kSqrt2OverPi = 0.79788456080286536f, kGeluCubic = 0.044715f;
+
+__device__ __forceinline__ float sigmoidf(float x) { return 1.0f / (1.0f + __expf(-x)); }
+
+__device__ __forceinline__ float act_value(float g, int act) {
+    if (act == ACT_SILU) return g * sigmoidf(g);
+    if (act == ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    // (1 + tanh z) / 2 = sigmoid(2 z)
+    return g * sigmoidf(2.0f * kSqrt2OverPi * (g + kGeluCubic * g * g * g));
+}
+
+__device__ __forceinline__ void act_slope(float g, int act, float& a, float& d) {
+    if (act == ACT_SILU) {
+        const float p = sigmoidf(g);
+        a = g * p;
+        d = p * (1.0f + g * (1.0f - p));
+    } else if (act == ACT_GELU) {
+        const float p = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+        a = g * p;
+        d = p + g * __expf(-0.5f * g * g) * 0.39894228040143268f;
+    } else {
+        const float p = sigmoidf(2.0f * kSqrt2OverPi * (g + kGeluCubic * g * g * g));
+        a = g * p;
+        d = p + g * p * (1.0f - p) * (2.0f * kSqrt2OverPi) * (1.0f + 3.0f * kGeluCubic * g * g);
+    }
+}
+
+}  // namespace bgf

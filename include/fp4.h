@@ -16,7 +16,9 @@
  *  - the GEMM on the quantized operands, one call, fp32 accumulation (the QuTLASS kernel list
  *    of the Quartet notes: 4-bit GEMM, online quantization of the output);
  *  - the key / value cache in the same E4M3 + E8M0 blocks: quantized as it is written, read back, and
- *    attention over it (own section at the end).
+ *    attention over it (own section);
+ *  - what stands between a layer's products: the root-mean-square norm, rotary positions and the gated
+ *    feed-forward, with their backward passes (own section at the end).
  *
  * Conventions for every entry point:
  *  - Pointers named x, y, codes, scales, tensor_scale, C and workspace are DEVICE pointers
@@ -400,6 +402,139 @@ int fp4_kv_attention_plan(const fp4_kv_cache* cache, const fp4_kv_batch* batch, 
 int64_t fp4_kv_attention_workspace_bytes(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv_attn* a);
 int fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const fp4_kv_attn* a, void* workspace,
                      int64_t ws_bytes, void* stream);
+
+/* ---- Between a layer's products: norm, rotary positions, gated feed-forward ---------------------
+ *
+ * Tensors here are row-major, fp32 or bf16 (`dtype`, one for every tensor of a call unless said
+ * otherwise), pointers 16-byte aligned, pitches in elements and multiples of 16 bytes. Sums and what is
+ * computed in between are fp32; a result is rounded once, as it is stored. rows == 0 (tokens == 0)
+ * queues nothing and returns FP4_OK. Every value comes from one thread's fixed order of operations (no
+ * atomics): the same call gives the same bits.
+ *
+ * Low-bit outputs: where out_q is not NULL, *q receives the fp32 result, before it is rounded to
+ * `dtype`, quantized along its rows as fp4_quantize would quantize it: E2M1 or E4M3 elements, (1, 32)
+ * groups, E8M0 floor or ceil scales, nearest even or stochastic (keyed by row * columns + column),
+ * rotated first where out_q->hadamard_n says so. q->codes (16-byte aligned) and q->scales are the
+ * caller's; q's other members are set to what was written. out_q and q are given together or not at all.
+ * Outputs must not overlap inputs or one another, but for the places that are named. */
+
+/* Root-mean-square norm of the rows of s = x + residual (of x where residual is NULL):
+ *   s = RN(x + residual) to dtype, stored to sum;  y = s / sqrt(mean(s^2) + eps) * weight
+ * What is normed is what sum holds. residual and sum: both or neither; sum may be x or residual themselves
+ * (then of the same pitch), y may be x. weight [cols], of w_dtype, or NULL for ones. y may be NULL where
+ * out_q is given. cols: a multiple of 8 up to 32768 (of 32, and of hadamard_n, with out_q); rows below
+ * 2^31. Sums of squares that leave fp32's range are outside the contract. */
+typedef struct fp4_norm {
+    const void* x;
+    const void* residual;
+    const void* weight;
+    void* sum;
+    void* y;
+    int64_t rows, cols;
+    int64_t ldx, ldr, lds, ldy;
+    int32_t dtype;
+    int32_t w_dtype;
+    float eps;
+} fp4_norm;
+int fp4_rmsnorm(const fp4_norm* n, const fp4_qparams* out_q, fp4_qtensor* y_q, void* stream);
+
+/* Its backward pass. s: what was normed (sum, or x); dy: the gradient of y; dsum: the gradient that
+ * reaches sum from elsewhere (the residual stream), or NULL. With r = 1 / sqrt(mean(s^2) + eps), n = s r
+ * and a = dy * weight:
+ *   dx = dsum + r (a - n mean(a n))      the gradient of x and of residual alike
+ *   dweight = sum over the rows of dy n  fp32 [cols], or NULL
+ * dx may be dy or dsum themselves (then of the same pitch). cols and rows as above. rows == 0 sets dweight
+ * to zeros. workspace: fp4_rmsnorm_backward_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0,
+ * -1 for arguments that the call would reject): partial sums of dweight, added in a fixed order. */
+typedef struct fp4_norm_grad {
+    const void* dy;
+    const void* s;
+    const void* dsum;
+    const void* weight;
+    void* dx;
+    float* dweight;
+    int64_t rows, cols;
+    int64_t lddy, lds, lddsum, lddx;
+    int32_t dtype;
+    int32_t w_dtype;
+    float eps;
+} fp4_norm_grad;
+int64_t fp4_rmsnorm_backward_workspace_bytes(const fp4_norm_grad* n);
+int fp4_rmsnorm_backward(const fp4_norm_grad* n, void* workspace, int64_t ws_bytes, void* stream);
+
+/* Rotary positions of up to two tensors [tokens, heads, head_dim] at once (queries and keys; heads[1] == 0:
+ * one tensor). Of each head the channels [0, rotary_dim) are turned in pairs, pair i being channels
+ * (i, i + rotary_dim / 2) in the half layout and (2 i, 2 i + 1) in the interleaved one:
+ *   (y1, y2) = scale * (x1 cos t - x2 sin t, x2 cos t + x1 sin t),  t = position * inv_freq[i]
+ * and the others are copied. backward != 0 turns by -t: the gradient of x from that of y. inv_freq: device
+ * fp64 [rotary_dim / 2], so that any scaling for long contexts is a table made once; the angle and its
+ * reduction are fp64, sine and cosine fp32 (2^-22 off at most).
+ * Positions: int32 [tokens] (positions), or those of a cache's batch (batch: of the batch's fields cu_tokens,
+ * context, seqs and tokens are used): row i of a sequence with n rows sits at context - n + i. Rows with no
+ * token (before a sequence's first, behind the last sequence) are left as they are. Exactly one of the two
+ * is given. out[i] may be x[i] itself (then of the same strides). Strides as for fp4_kv_append. head_dim up
+ * to 1024, rotary_dim even, at most head_dim; tokens * heads below 2^31. */
+enum { FP4_ROPE_HALF = 0, FP4_ROPE_INTERLEAVED = 1 };
+typedef struct fp4_rope_args {
+    const void* x[2];
+    void* out[2];
+    int64_t ldx[2], ldx_head[2];
+    int64_t ldo[2], ldo_head[2];
+    int32_t heads[2];
+    int64_t tokens;
+    const double* inv_freq;
+    const int32_t* positions;
+    const fp4_kv_batch* batch;
+    float scale;
+    int32_t dtype;
+    int32_t head_dim;
+    int32_t rotary_dim;
+    int32_t layout;
+    int32_t backward;
+} fp4_rope_args;
+int fp4_rope(const fp4_rope_args* a, void* stream);
+
+/* Gated feed-forward on quantized operands, A [M, K], gate and up [F, K]:
+ *   g = A gate^T, u = A up^T (fp32 accumulation),  h = act(g) * u
+ * in one pass over the operands. Operand pairs as for fp4_gemm without NVFP4: MXFP4 (the weights may use
+ * (32, 32) tiles) or MXFP8; gate and up share one set of parameters, and A's rotation. h [M, F] and gu
+ * [M, 2 F] (g, then u: what fp4_gated_backward reads) of dtype, either may be NULL; out_q / h_q as above with
+ * hadamard_n <= 128 and F % 32 == 0; at least one of the three outputs. Pitches need not be multiples of
+ * 16 bytes (that only narrows the stores).
+ * act: x / (1 + e^-x); x Phi(x) with the error function; the same with
+ * Phi(x) ~ (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2.
+ * How the work is tiled changes the order of the sums, never what is meant. workspace:
+ * fp4_gemm_gated_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0; -1 for arguments that the
+ * call would reject; only M, F, K, the parameters, dtype and out_q matter): h in fp32 where a rotation spans
+ * more columns than a tile. */
+enum { FP4_ACT_SILU = 0, FP4_ACT_GELU = 1, FP4_ACT_GELU_TANH = 2 };
+typedef struct fp4_gated {
+    void* h;
+    void* gu;
+    int64_t ldh, ldgu;
+    int32_t dtype;
+    int32_t act;
+} fp4_gated;
+int64_t fp4_gemm_gated_workspace_bytes(const fp4_qtensor* A, const fp4_qtensor* gate, const fp4_qtensor* up,
+                                       const fp4_gated* o, const fp4_qparams* out_q);
+int fp4_gemm_gated(const fp4_qtensor* A, const fp4_qtensor* gate, const fp4_qtensor* up, const fp4_gated* o,
+                   const fp4_qparams* out_q, fp4_qtensor* h_q, void* workspace, int64_t ws_bytes, void* stream);
+
+/* Gradients of its two products from dh [rows, F] and gu [rows, 2 F]:
+ *   dgu = (dh * u * act'(g), dh * act(g)) [rows, 2 F]
+ * and, with out_q, dgu quantized along its 2 F columns: the operand of dA = dgu [gate; up]. dgu may be NULL
+ * where out_q is given, and may be gu itself (then of the same pitch). F: a multiple of 8 (of 32, and of
+ * hadamard_n, with out_q). */
+typedef struct fp4_gated_grad {
+    const void* dh;
+    const void* gu;
+    void* dgu;
+    int64_t rows, cols; /* cols = F */
+    int64_t lddh, ldgu, lddgu;
+    int32_t dtype;
+    int32_t act;
+} fp4_gated_grad;
+int fp4_gated_backward(const fp4_gated_grad* g, const fp4_qparams* out_q, fp4_qtensor* dgu_q, void* stream);
 
 #ifdef __cplusplus
 }
