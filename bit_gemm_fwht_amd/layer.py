@@ -17,7 +17,6 @@ and for training
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 from typing import NamedTuple
 
@@ -44,10 +43,11 @@ class NormGradC(ctypes.Structure):
 
 
 class RopeC(ctypes.Structure):
-    _fields_ = [("x", _P * 2), ("out", _P * 2), ("ldx", _I64 * 2), ("ldx_head", _I64 * 2), ("ldo", _I64 * 2),
-                ("ldo_head", _I64 * 2), ("heads", _I32 * 2), ("tokens", _I64), ("inv_freq", _P), ("positions", _P),
-                ("batch", _P), ("scale", _F), ("dtype", _I32), ("head_dim", _I32), ("rotary_dim", _I32), ("layout", _I32),
-                ("backward", _I32)]
+    # the pairs of the C struct member by member: tuples take longer to convert than the rest of a call
+    _fields_ = [("x0", _P), ("x1", _P), ("out0", _P), ("out1", _P), ("ldx0", _I64), ("ldx1", _I64), ("ldx_head0", _I64),
+                ("ldx_head1", _I64), ("ldo0", _I64), ("ldo1", _I64), ("ldo_head0", _I64), ("ldo_head1", _I64),
+                ("heads0", _I32), ("heads1", _I32), ("tokens", _I64), ("inv_freq", _P), ("positions", _P), ("batch", _P),
+                ("scale", _F), ("dtype", _I32), ("head_dim", _I32), ("rotary_dim", _I32), ("layout", _I32), ("backward", _I32)]
 
 
 class GatedC(ctypes.Structure):
@@ -79,60 +79,95 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_CODES = kv._CODES
 _code, _stream, _check = kv._code, kv._stream, kv._check
 
 
-def _matrix(t: torch.Tensor, rows, cols, dtype, dev, name: str) -> None:
-    """Check a row-major [rows, cols] CUDA tensor (None: any) of dtype on dev."""
-    shape = t.shape
-    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
-        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'cols' if cols is None else cols}], not {tuple(shape)}")
-    if not t.is_cuda or t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev if dev.type == 'cuda' else 'a CUDA device'}")
-    if t.dtype != dtype:
+# Small calls last as long as their host side, so a check first asks, in as few calls as there are, whether all is
+# well; _refuse says what is not.
+
+def _matrix(t: torch.Tensor, shape, dtype, index: int, name: str) -> int:
+    """Check a row-major CUDA tensor of this shape and dtype on device `index`; returns its pitch."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == index and index >= 0:
+        ld, step = t.stride()
+        if step == 1 or shape[1] <= 1:
+            return ld if shape[0] > 1 else shape[1]
+    _refuse(t, shape, dtype, index, name)
+
+
+def _refuse(t: torch.Tensor, shape, dtype, index: int, name: str):
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on {f'cuda:{index}' if index >= 0 else 'a CUDA device'}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
-    if shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be contiguous along its last axis")
+    raise ValueError(f"{name} must be contiguous along its last axis")
 
 
-def _pitch(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _first(t: torch.Tensor, name: str):
+    """Shape, dtype code, device index and pitch of the matrix that the others of a call are held to."""
+    code = _CODES.get(t.dtype)
+    if code is None:
+        _code(t.dtype, name)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be [rows, cols], not {list(shape)}")
+    index = t.get_device()
+    return shape, code, index, _matrix(t, shape, t.dtype, index, name)
 
 
-def _vector(t: torch.Tensor, n: int, dev, name: str) -> None:
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [{n}] tensor, not {tuple(t.shape)}")
-    fp4._on(dev, t)
+def _vector(t: torch.Tensor, n: int, index: int, name: str) -> None:
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] tensor, not {list(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
 
-@functools.lru_cache(maxsize=256)
+def _new(rows: int, cols: int, dtype, dev) -> torch.Tensor:
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=dev)
+
+
 def _params_c(p: Params):
-    """The library's form of frozen parameters (read by it, never written) and its address; a call holds the pair."""
-    c = p.c()
-    return c, ctypes.addressof(c)
+    """The library's form of parameters, which are frozen: made once and kept with them."""
+    c = p.__dict__.get("_c")
+    if c is None:
+        c = p.c()
+        object.__setattr__(p, "_c", c)
+    return c
 
 
-def _rows(t: torch.Tensor, heads, dim: int, dev, name: str) -> int:
-    """Check [tokens, heads, dim] rows of bf16 / fp32 on dev; returns the dtype code."""
-    code = _code(t.dtype, name)
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the rotary table on {dev}")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [tokens, {heads if heads is not None else 'heads'}, {dim}], not {tuple(t.shape)}")
-    if t.stride(2) != 1:
-        raise ValueError(f"{name} must be contiguous along its last axis")
-    return code
+# The current device's index; the public call initialises CUDA first if need be, which takes twice as long.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _quant_out(rows: int, cols: int, params: Params, dev, q_out, name: str = "q_out") -> QTensor:
+def _there(index: int, call, *args, **kw):
+    """The call with its tensors' device current: kernels and limits belong to the current device."""
+    with torch.cuda.device(index):
+        return call(*args, **kw)
+
+
+def _codes(q: QTensor, rows: int, cols: int, params: Params, index: int, name: str) -> None:
+    """Check that q's buffers hold a [rows, cols] tensor with one scale a block (of E8M0, the only ones here)."""
+    n = rows * cols
+    b = params.block
+    for t, need, what in ((q.codes, n >> 1 if params.elem == fp4.E2M1 else n, "codes"),
+                          (q.scales, n // (b[0] * b[1]), "scales")):
+        if t.get_device() != index:
+            raise ValueError(f"{name}.{what} is on {t.device}, not on cuda:{index}")
+        if not t.is_contiguous() or t.numel() * t.element_size() < need:
+            raise ValueError(f"{name}.{what} must be contiguous and hold at least {need} bytes")
+
+
+def _quant_out(rows: int, cols: int, params: Params, dev, index: int, q_out) -> QTensor:
+    if q_out is not None:
+        _codes(q_out, rows, cols, params, index, "q_out")
+        return q_out
     if rows == 0:
         def none():
             return torch.empty(0, dtype=torch.uint8, device=dev)
-        return q_out if q_out is not None else QTensor(none(), none(), None, 0, cols, params)
-    if q_out is None:
-        return fp4.empty_qtensor(rows, cols, params, dev)
-    fp4._check_q(q_out, rows, cols, params, dev, name)
-    return q_out
+        return QTensor(none(), none(), None, 0, cols, params)
+    return fp4.empty_qtensor(rows, cols, params, dev)
 
 
 def _quant_c(q: QTensor):
@@ -145,13 +180,10 @@ def _describe(q: QTensor, rows: int, cols: int, params: Params) -> None:
 
 
 def _workspace(workspace, need: int, dev):
-    if need <= 0:
-        return None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    else:
-        fp4._ws_bytes(workspace, need, dev)
-    return workspace, need
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    fp4._ws_bytes(workspace, need, dev)
+    return workspace
 
 
 class Normed(NamedTuple):
@@ -167,42 +199,43 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e
     of x + residual, which is stored too (to sum_out: x or residual themselves, or a new tensor). weight [cols]
     bf16 / fp32. out_q: quantize the output (groups of 32, E8M0 scales; rotated with out_q.hadamard_n);
     keep_y=False then skips y itself."""
-    dev = x.device
-    code = _code(x.dtype, "x")
-    _matrix(x, None, None, x.dtype, dev, "x")
-    rows, cols = x.shape
-    w_code = 0
+    shape, code, index, ldx = _first(x, "x")
+    if index != _device():
+        return _there(index, rmsnorm, x, weight, eps, residual, out, sum_out, out_q, q_out, keep_y)
+    rows, cols = shape
+    dtype, dev = x.dtype, x.device
+    w_code = ldr = lds = ldy = 0
+    w = r = s = y = None
     if weight is not None:
-        _vector(weight, cols, dev, "weight")
-        w_code = _code(weight.dtype, "weight")
+        _vector(weight, cols, index, "weight")
+        w_code, w = _code(weight.dtype, "weight"), weight.data_ptr()
     if residual is not None:
-        _matrix(residual, rows, cols, x.dtype, dev, "residual")
+        ldr, r = _matrix(residual, shape, dtype, index, "residual"), residual.data_ptr()
         if sum_out is None:
-            sum_out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+            sum_out, lds = _new(rows, cols, dtype, dev), cols
         else:
-            _matrix(sum_out, rows, cols, x.dtype, dev, "sum_out")
+            lds = _matrix(sum_out, shape, dtype, index, "sum_out")
+        s = sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out goes with a residual")
-    if out_q is None and not keep_y:
-        raise ValueError("keep_y=False goes with out_q")
     if out is not None:
-        _matrix(out, rows, cols, x.dtype, dev, "out")
+        ldy, y = _matrix(out, shape, dtype, index, "out"), out.data_ptr()
     elif keep_y:
-        out = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-    c = NormC(x.data_ptr(), None if residual is None else residual.data_ptr(), None if weight is None else weight.data_ptr(),
-              None if sum_out is None else sum_out.data_ptr(), None if out is None else out.data_ptr(), rows, cols, _pitch(x),
-              0 if residual is None else _pitch(residual), 0 if sum_out is None else _pitch(sum_out),
-              0 if out is None else _pitch(out), code, w_code, eps)
-    qp = qa = qc = None
+        out, ldy = _new(rows, cols, dtype, dev), cols
+        y = out.data_ptr()
+    elif out_q is None:
+        raise ValueError("keep_y=False goes with out_q")
+    c = NormC(x.data_ptr(), r, w, s, y, rows, cols, ldx, ldr, lds, ldy, code, w_code, eps)
+    qp = qa = None
     if out_q is not None:
-        q_out = _quant_out(rows, cols, out_q, dev, q_out)
-        held = _params_c(out_q)
-        qp = held[1]
-        qc = _quant_c(q_out)
+        q_out = _quant_out(rows, cols, out_q, dev, index, q_out)
+        qp, qc = ctypes.addressof(_params_c(out_q)), _quant_c(q_out)
         qa = ctypes.addressof(qc)
     elif q_out is not None:
         raise ValueError("q_out goes with out_q")
-    _check(lib().fp4_rmsnorm(ctypes.addressof(c), qp, qa, _stream(dev)), "fp4_rmsnorm")
+    st = lib().fp4_rmsnorm(ctypes.addressof(c), qp, qa, _stream(dev))
+    if st:
+        _check(st, "fp4_rmsnorm")
     if q_out is not None:
         _describe(q_out, rows, cols, out_q)
     return Normed(out, sum_out, q_out)
@@ -215,35 +248,41 @@ def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor | N
     or x), dsum the gradient that reaches it from the residual stream. dx is the gradient of x and of the
     residual alike (out: dy or dsum themselves, or a new tensor). dweight: True for a new fp32 [cols], a tensor
     to write to, or False for none (a frozen weight)."""
-    dev = dy.device
-    code = _code(dy.dtype, "dy")
-    _matrix(dy, None, None, dy.dtype, dev, "dy")
-    rows, cols = dy.shape
-    _matrix(s, rows, cols, dy.dtype, dev, "s")
-    w_code = 0
+    shape, code, index, lddy = _first(dy, "dy")
+    if index != _device():
+        return _there(index, rmsnorm_backward, dy, s, weight, eps, dsum, out, dweight, workspace)
+    rows, cols = shape
+    dtype, dev = dy.dtype, dy.device
+    lds = _matrix(s, shape, dtype, index, "s")
+    w_code = lddsum = 0
+    w = ds = None
     if weight is not None:
-        _vector(weight, cols, dev, "weight")
-        w_code = _code(weight.dtype, "weight")
+        _vector(weight, cols, index, "weight")
+        w_code, w = _code(weight.dtype, "weight"), weight.data_ptr()
     if dsum is not None:
-        _matrix(dsum, rows, cols, dy.dtype, dev, "dsum")
+        lddsum, ds = _matrix(dsum, shape, dtype, index, "dsum"), dsum.data_ptr()
     if out is None:
-        out = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
+        out, lddx = _new(rows, cols, dtype, dev), cols
     else:
-        _matrix(out, rows, cols, dy.dtype, dev, "out")
+        lddx = _matrix(out, shape, dtype, index, "out")
     if dweight is True:
-        dweight = torch.empty(cols, dtype=torch.float32, device=dev)
+        dweight = torch.empty_strided((cols,), (1,), dtype=torch.float32, device=dev)
     elif dweight is False:
         dweight = None
-    if dweight is not None:
-        _vector(dweight, cols, dev, "dweight")
-        if dweight.dtype != torch.float32:
+    elif dweight is not None:
+        _vector(dweight, cols, index, "dweight")
+        if dweight.dtype is not torch.float32:
             raise TypeError("dweight must be float32")
-    c = NormGradC(dy.data_ptr(), s.data_ptr(), None if dsum is None else dsum.data_ptr(),
-                  None if weight is None else weight.data_ptr(), out.data_ptr(), None if dweight is None else dweight.data_ptr(),
-                  rows, cols, _pitch(dy), _pitch(s), 0 if dsum is None else _pitch(dsum), _pitch(out), code, w_code, eps)
+    c = NormGradC(dy.data_ptr(), s.data_ptr(), ds, w, out.data_ptr(), None if dweight is None else dweight.data_ptr(), rows, cols,
+                  lddy, lds, lddsum, lddx, code, w_code, eps)
     L, pc = lib(), ctypes.addressof(c)
-    ws, need = _workspace(workspace, L.fp4_rmsnorm_backward_workspace_bytes(pc), dev)
-    _check(L.fp4_rmsnorm_backward(pc, None if ws is None else ws.data_ptr(), need, _stream(dev)), "fp4_rmsnorm_backward")
+    need, ws = L.fp4_rmsnorm_backward_workspace_bytes(pc), None
+    if need > 0:
+        workspace = _workspace(workspace, need, dev)
+        ws = workspace.data_ptr()
+    st = L.fp4_rmsnorm_backward(pc, ws, need, _stream(dev))
+    if st:
+        _check(st, "fp4_rmsnorm_backward")
     return out, dweight
 
 
@@ -311,7 +350,7 @@ class Rotary:
             raise ValueError("layout must be HALF or INTERLEAVED")
         self.inv_freq, self.layout, self.scale, self.device = inv_freq, layout, float(scale), inv_freq.device
         self.rotary_dim = 2 * inv_freq.shape[0]
-        self._ptr = inv_freq.data_ptr()
+        self._ptr, self._index = inv_freq.data_ptr(), inv_freq.get_device()
 
 
 def rope(x, rotary: Rotary, positions, out=None, backward: bool = False):
@@ -319,46 +358,66 @@ def rope(x, rotary: Rotary, positions, out=None, backward: bool = False):
     dtype and head_dim) in one launch; strides of whole 16 bytes. positions: int32 [tokens], or the kv.Batch of a cache (a
     sequence's rows are its last ones; rows with no token keep what `out` held). out: a tensor (pair) to write to,
     x itself for in place. backward=True turns the other way: the gradient of x from that of the result."""
-    pair = isinstance(x, (tuple, list))
-    xs = x if pair else (x,)
-    if pair and len(xs) != 2:
-        raise ValueError("x must be a tensor or a pair of tensors")
-    first, dev = xs[0], rotary.device
-    tokens, dim = first.shape[0], first.shape[-1]
-    code = _rows(first, None, dim, dev, "x")
-    if pair and (_rows(xs[1], None, dim, dev, "x[1]") != code or xs[1].shape[0] != tokens):
-        raise ValueError("both tensors must have one dtype and one number of tokens")
+    pair = not isinstance(x, torch.Tensor)
+    a, b = x if pair else (x, None)
+    index, dev = rotary._index, rotary.device
+    if index != _device():
+        return _there(index, rope, x, rotary, positions, out, backward)
+    dtype = a.dtype
+    code = _CODES.get(dtype)
+    if code is None:
+        _code(dtype, "x")
+    tokens, heads, dim = _heads(a, tokens=None, dim=None, dtype=dtype, index=index, name="x")
+    heads_b = _heads(b, tokens, dim, dtype, index, "x[1]")[1] if pair else 0
     if out is None:
-        outs = tuple(torch.empty(t.shape, dtype=t.dtype, device=dev) for t in xs)
+        o = torch.empty_strided((tokens, heads, dim), (heads * dim, dim, 1), dtype=dtype, device=dev)
+        p = torch.empty_strided((tokens, heads_b, dim), (heads_b * dim, dim, 1), dtype=dtype, device=dev) if pair else None
     else:
-        outs = tuple(out) if pair else (out,)
-        if len(outs) != len(xs):
-            raise ValueError("out must be given like x")
-        for t, o in zip(xs, outs):
-            if _rows(o, t.shape[1], dim, dev, "out") != code or o.shape[0] != tokens:
+        o, p = out if pair else (out, None)
+        for t, n in ((o, heads), (p, heads_b)):
+            if t is not None and _heads(t, tokens, dim, dtype, index, "out")[1] != n:
                 raise ValueError("out must have x's shape and dtype")
     pos = batch = None
     if isinstance(positions, kv.Batch):
         if positions.device != dev:
-            raise ValueError(f"the batch is on {positions.device}, x on {dev}")
+            raise ValueError(f"the batch is on {positions.device}, the rotary table on {dev}")
         held = positions._at(tokens)  # alive until the call has returned
         batch = held[1]
     else:
-        if positions.dtype != torch.int32:
+        _vector(positions, tokens, index, "positions")
+        if positions.dtype is not torch.int32:
             raise TypeError("positions must be int32")
-        _vector(positions, tokens, dev, "positions")
         pos = positions.data_ptr()
-    a, o = xs[0], outs[0]
+    x_ld, x_head, _ = a.stride()
+    o_ld, o_head, _ = o.stride()
     if pair:
-        b, p = xs[1], outs[1]
-        c = RopeC((a.data_ptr(), b.data_ptr()), (o.data_ptr(), p.data_ptr()), (a.stride(0), b.stride(0)), (a.stride(1), b.stride(1)),
-                  (o.stride(0), p.stride(0)), (o.stride(1), p.stride(1)), (a.shape[1], b.shape[1]), tokens, rotary._ptr, pos, batch,
-                  rotary.scale, code, dim, rotary.rotary_dim, rotary.layout, backward)
+        x1, y1 = b.data_ptr(), p.data_ptr()
+        x1_ld, x1_head, _ = b.stride()
+        o1_ld, o1_head, _ = p.stride()
     else:
-        c = RopeC((a.data_ptr(),), (o.data_ptr(),), (a.stride(0),), (a.stride(1),), (o.stride(0),), (o.stride(1),), (a.shape[1],),
-                  tokens, rotary._ptr, pos, batch, rotary.scale, code, dim, rotary.rotary_dim, rotary.layout, backward)
-    _check(lib().fp4_rope(ctypes.addressof(c), _stream(dev)), "fp4_rope")
-    return outs if pair else outs[0]
+        x1 = y1 = None
+        x1_ld = x1_head = o1_ld = o1_head = 0
+    c = RopeC(a.data_ptr(), x1, o.data_ptr(), y1, x_ld, x1_ld, x_head, x1_head, o_ld, o1_ld, o_head, o1_head, heads, heads_b, tokens,
+              rotary._ptr, pos, batch, rotary.scale, code, dim, rotary.rotary_dim, rotary.layout, backward)
+    st = lib().fp4_rope(ctypes.addressof(c), _stream(dev))
+    if st:
+        _check(st, "fp4_rope")
+    return (o, p) if pair else o
+
+
+def _heads(t: torch.Tensor, tokens, dim, dtype, index: int, name: str):
+    """Check [tokens, heads, dim] rows (None: any) of dtype on device `index`; returns their shape."""
+    shape = t.shape
+    if len(shape) != 3 or (tokens is not None and shape[0] != tokens) or (dim is not None and shape[2] != dim):
+        raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}, heads, {'head_dim' if dim is None else dim}], "
+                         f"not {list(shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the rotary table on cuda:{index}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    return shape
 
 
 class GatedWeights:
@@ -377,6 +436,7 @@ class GatedWeights:
         for q, name in ((gate, "gate"), (up, "up")):
             fp4._check_q(q, q.rows, q.cols, q.params, self.device, name)
         self.gate, self.up, self.act, self.ff, self.hidden = gate, up, act, gate.rows, gate.cols
+        self._index = gate.codes.get_device()
         self._c = gate.c(), up.c()
         self._p = tuple(ctypes.addressof(c) for c in self._c)
 
@@ -404,38 +464,48 @@ def gated(a: QTensor, weights: GatedWeights, out_dtype=torch.bfloat16, out: torc
     """act(a gate^T) * (a up^T) of a [rows, K] in one pass (fp32 accumulation). keep_h=False skips h itself where
     out_q asks for its codes; keep_gu: True for a new [rows, 2 F] tensor of out_dtype with both products, or one to
     write to."""
-    dev, rows, ff = weights.device, a.rows, weights.ff
-    if a.cols != weights.hidden:
-        raise ValueError(f"a has {a.cols} columns, the weights {weights.hidden}")
-    if rows > 0:
-        fp4._check_q(a, rows, a.cols, a.params, dev, "a")
-    code = _code(out_dtype if out is None else out.dtype, "out")
+    dev, index, rows, ff, cols = weights.device, weights._index, a.rows, weights.ff, a.cols
+    if index != _device():
+        return _there(index, gated, a, weights, out_dtype, out, keep_h, keep_gu, out_q, q_out, workspace)
+    if cols != weights.hidden:
+        raise ValueError(f"a has {cols} columns, the weights {weights.hidden}")
+    _codes(a, rows, cols, a.params, index, "a")
     dtype = out_dtype if out is None else out.dtype
+    code = _CODES.get(dtype)
+    if code is None:
+        _code(dtype, "out")
+    h = p = None
+    ldh = ldgu = 0
     if out is not None:
-        _matrix(out, rows, ff, dtype, dev, "out")
+        ldh, h = _matrix(out, (rows, ff), dtype, index, "out"), out.data_ptr()
     elif keep_h:
-        out = torch.empty((rows, ff), dtype=dtype, device=dev)
+        out, ldh = _new(rows, ff, dtype, dev), ff
+        h = out.data_ptr()
     gu = None
     if keep_gu is True:
-        gu = torch.empty((rows, 2 * ff), dtype=dtype, device=dev)
+        gu, ldgu = _new(rows, 2 * ff, dtype, dev), 2 * ff
+        p = gu.data_ptr()
     elif keep_gu is not False and keep_gu is not None:
         gu = keep_gu
-        _matrix(gu, rows, 2 * ff, dtype, dev, "keep_gu")
-    c = GatedC(None if out is None else out.data_ptr(), None if gu is None else gu.data_ptr(), 0 if out is None else _pitch(out),
-               0 if gu is None else _pitch(gu), code, weights.act)
-    qp = qa = qc = None
+        ldgu, p = _matrix(gu, (rows, 2 * ff), dtype, index, "keep_gu"), gu.data_ptr()
+    c = GatedC(h, p, ldh, ldgu, code, weights.act)
+    ac = fp4.QTensorC(a.codes.data_ptr(), a.scales.data_ptr(), None, rows, cols, _params_c(a.params))
+    L, pa, po, (pg, pu) = lib(), ctypes.addressof(ac), ctypes.addressof(c), weights._p
+    qp = qa = ws = None
+    need = 0
     if out_q is not None:
-        q_out = _quant_out(rows, ff, out_q, dev, q_out)
-        held = _params_c(out_q)
-        qp = held[1]
-        qc = _quant_c(q_out)
+        q_out = _quant_out(rows, ff, out_q, dev, index, q_out)
+        qp, qc = ctypes.addressof(_params_c(out_q)), _quant_c(q_out)
         qa = ctypes.addressof(qc)
+        need = L.fp4_gemm_gated_workspace_bytes(pa, pg, pu, po, qp)  # there is none without out_q
+        if need > 0:
+            workspace = _workspace(workspace, need, dev)
+            ws = workspace.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out goes with out_q")
-    ac = fp4.QTensorC(a.codes.data_ptr(), a.scales.data_ptr(), None, rows, a.cols, _params_c(a.params)[0])
-    L, pa, po, (pg, pu) = lib(), ctypes.addressof(ac), ctypes.addressof(c), weights._p
-    ws, need = _workspace(workspace, L.fp4_gemm_gated_workspace_bytes(pa, pg, pu, po, qp), dev)
-    _check(L.fp4_gemm_gated(pa, pg, pu, po, qp, qa, None if ws is None else ws.data_ptr(), need, _stream(dev)), "fp4_gemm_gated")
+    st = L.fp4_gemm_gated(pa, pg, pu, po, qp, qa, ws, need, _stream(dev))
+    if st:
+        _check(st, "fp4_gemm_gated")
     if q_out is not None:
         _describe(q_out, rows, ff, out_q)
     return Gated(out, q_out, gu)
@@ -450,29 +520,31 @@ def gated_backward(dh: torch.Tensor, gu: torch.Tensor, act: int = SILU, out: tor
                    out_q: Params | None = None, q_out: QTensor | None = None) -> GatedGrad:
     """Gradients of gated()'s two products from dh [rows, F] and the gu [rows, 2 F] it kept (out: gu itself, or a
     new tensor). keep=False skips dgu itself where out_q asks for its codes."""
-    dev = dh.device
-    code = _code(dh.dtype, "dh")
-    _matrix(dh, None, None, dh.dtype, dev, "dh")
-    rows, ff = dh.shape
-    _matrix(gu, rows, 2 * ff, dh.dtype, dev, "gu")
-    if out_q is None and not keep:
-        raise ValueError("keep=False goes with out_q")
+    shape, code, index, lddh = _first(dh, "dh")
+    if index != _device():
+        return _there(index, gated_backward, dh, gu, act, out, keep, out_q, q_out)
+    rows, ff = shape
+    dtype, dev, wide = dh.dtype, dh.device, (rows, 2 * ff)
+    ldgu = _matrix(gu, wide, dtype, index, "gu")
+    lddgu, p = 0, None
     if out is not None:
-        _matrix(out, rows, 2 * ff, dh.dtype, dev, "out")
+        lddgu, p = _matrix(out, wide, dtype, index, "out"), out.data_ptr()
     elif keep:
-        out = torch.empty((rows, 2 * ff), dtype=dh.dtype, device=dev)
-    c = GatedGradC(dh.data_ptr(), gu.data_ptr(), None if out is None else out.data_ptr(), rows, ff, _pitch(dh), _pitch(gu),
-                   0 if out is None else _pitch(out), code, act)
-    qp = qa = qc = None
+        out, lddgu = _new(rows, 2 * ff, dtype, dev), 2 * ff
+        p = out.data_ptr()
+    elif out_q is None:
+        raise ValueError("keep=False goes with out_q")
+    c = GatedGradC(dh.data_ptr(), gu.data_ptr(), p, rows, ff, lddh, ldgu, lddgu, code, act)
+    qp = qa = None
     if out_q is not None:
-        q_out = _quant_out(rows, 2 * ff, out_q, dev, q_out)
-        held = _params_c(out_q)
-        qp = held[1]
-        qc = _quant_c(q_out)
+        q_out = _quant_out(rows, 2 * ff, out_q, dev, index, q_out)
+        qp, qc = ctypes.addressof(_params_c(out_q)), _quant_c(q_out)
         qa = ctypes.addressof(qc)
     elif q_out is not None:
         raise ValueError("q_out goes with out_q")
-    _check(lib().fp4_gated_backward(ctypes.addressof(c), qp, qa, _stream(dev)), "fp4_gated_backward")
+    st = lib().fp4_gated_backward(ctypes.addressof(c), qp, qa, _stream(dev))
+    if st:
+        _check(st, "fp4_gated_backward")
     if q_out is not None:
         _describe(q_out, rows, 2 * ff, out_q)
     return GatedGrad(out, q_out)

@@ -134,7 +134,8 @@ def rope(layer, batch=None, **kw):
              heads=(4, 2), tokens=3, inv_freq=0x50000, positions=None if batch else 0x60000, batch=batch, scale=1.0, dtype=1,
              head_dim=128, rotary_dim=64, layout=0, backward=0)
     a.update(kw)
-    return layer.RopeC(**a)
+    pairs = ("x", "out", "ldx", "ldx_head", "ldo", "ldo_head", "heads")
+    return layer.RopeC(**{k + str(i): a[k][i] for k in pairs for i in (0, 1)}, **{k: v for k, v in a.items() if k not in pairs})
 
 
 @pytest.mark.parametrize("kw,want", [
