@@ -2,12 +2,12 @@
 // two products kept (g | u) and h quantized along its columns; and its backward pass.
 //
 // Both products of a place are accumulated in the same lane's registers, so the activation and the product
-// need no exchange and g and u never leave the chip unless they are asked for. Two kernels:
+// need no exchange and g and u never leave the chip unless they are asked for. Three kernels:
 //  - k_gated_tile: the pipelined GEMM tile (gemm_tile.h) on B slabs that hold 32 rows of Wg and the same 32
 //    of Wu in turn: 256 x 128 or 128 x 64 results a workgroup;
-//  - k_gated_rows: few rows of A, and every K that the tiles do not take: 32 columns a workgroup, its waves
-//    each multiply a share of K straight from memory (no LDS: no weight is used twice), the shares are added
-//    through LDS in a fixed order.
+//  - k_gated_stream: up to 64 rows of A, K a multiple of 128: bound by the weights' bytes;
+//  - k_gated_rows: every other K: 32 columns a workgroup, its waves each multiply a share of K straight from
+//    memory, the shares are added through LDS in a fixed order.
 #include "device.h"
 #include "fp4_internal.h"
 #include "gemm_tile.h"
@@ -136,6 +136,221 @@ __global__ __launch_bounds__(TS == 256 ? 512 : 256, TS == 256 ? 1 : 2) void k_ga
     big_tile<FP8, B2D, OUT, false, FQ, TS, true>(g, tm, tn, smem);
 }
 
+// Store one place's values: gu, h, and h for a quantize pass of its own.
+template <int OUT>
+__device__ __forceinline__ void store_gated(const GemmArgs& g, int64_t row, int64_t col, float gv, float uv, float h) {
+    if constexpr (OUT == DT_F32) {
+        if (g.gu) {
+            float* d = reinterpret_cast<float*>(g.gu) + row * g.ldgu + col;
+            d[0] = gv;
+            d[g.N] = uv;
+        }
+        if (g.c) reinterpret_cast<float*>(g.c)[row * g.ldc + col] = h;
+    } else {
+        if (g.gu) {
+            uint16_t* d = reinterpret_cast<uint16_t*>(g.gu) + row * g.ldgu + col;
+            d[0] = (uint16_t)pack_bf16x2_rne(gv, 0.0f);
+            d[g.N] = (uint16_t)pack_bf16x2_rne(uv, 0.0f);
+        }
+        if (g.c) reinterpret_cast<uint16_t*>(g.c)[row * g.ldc + col] = (uint16_t)pack_bf16x2_rne(h, 0.0f);
+    }
+    if (g.h32) g.h32[row * g.N + col] = h;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Few rows, K a multiple of 128: bound by the weights' bytes. A workgroup of NW waves takes 16 NC columns of
+// both projections and up to 16 MT rows of A; wave w takes the 128-byte units w, w + NW, .. of K by itself: it
+// copies a unit's codes and scales straight into a ring of D buffers of its own in LDS (whole 128-byte runs of
+// memory a row, many in flight, no registers and no barrier) and multiplies them with 16x16x128 scaled products
+// (lane layouts in gemm.hip). The waves' shares of K are added through LDS in the order of the waves. Rows past
+// M and F lie past the buffers' extents and read as zeros without touching memory.
+// ---------------------------------------------------------------------------------------------
+constexpr int kStreamWaves = 4;
+
+template <bool FP8, int NC, int MT, int NW, int D>
+struct Stream {
+    static constexpr int WR = 16 * NC, AR = 16 * MT;      // rows of a projection, of A
+    static constexpr int SPR = FP8 ? 4 : 8;               // scale bytes of a row's unit
+    static constexpr int STEPS = FP8 ? 1 : 2;             // products of a unit
+    static constexpr int WSZ = (WR * SPR + 255) / 256 * 256;
+    static constexpr int OFF_U = WR * 128, OFF_A = 2 * WR * 128, OFF_SG = OFF_A + AR * 128, OFF_SU = OFF_SG + WSZ;
+    static constexpr int OFF_SA = OFF_SU + WSZ, ASZ = (AR * SPR + 255) / 256 * 256;
+    static constexpr int UNIT = OFF_SA + ASZ;             // bytes of a buffer
+    static constexpr int COPIES = 4 * NC + 2 * MT + (2 * WSZ + ASZ) / 256;  // vector-memory instructions of a unit
+    static constexpr int HP = WR + 4;                     // row pitch of the shares, in values
+    static constexpr int SHARE = 2 * AR * HP;             // values of a wave's share: g, then u
+    static constexpr int RING = NW * D * UNIT, SUM = 4 * NW * SHARE;
+    static constexpr int LDS = RING > SUM ? RING : SUM;
+    static_assert(LDS <= 160 * 1024, "LDS budget");
+};
+
+template <bool FP8, int OUT, int FQ, int NC, int MT, int NW, int D>
+__global__ __launch_bounds__(64 * NW) void k_gated_stream(GemmArgs g) {
+    using S = Stream<FP8, NC, MT, NW, D>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int fr = lane & 15, fq = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * S::WR, m0 = (int64_t)blockIdx.y * S::AR;
+    const int rowbytes = (int)(FP8 ? g.K : g.K / 2), kgroups = (int)(g.K / 32);
+    const int units = (rowbytes + 127) / 128, mine = (units - wave + NW - 1) / NW;
+    uint8_t* const ring = smem + wave * D * S::UNIT;
+
+    const int64_t srows = g.b_2d ? (g.N + 31) / 32 : g.N;
+    auto resource = [](const void* p, int64_t bytes) { return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000); };
+    const __amdgpu_buffer_rsrc_t rG = resource(g.b, g.N * rowbytes), rU = resource(g.b_up, g.N * rowbytes);
+    const __amdgpu_buffer_rsrc_t rA = resource(g.a, g.M * rowbytes), rSA = resource(g.sa, g.M * kgroups);
+    const __amdgpu_buffer_rsrc_t rSG = resource(g.sb, srows * kgroups), rSU = resource(g.sb_up, srows * kgroups);
+    // extent 0: units past the last read nothing, so that every unit is the same number of copies
+    const __amdgpu_buffer_rsrc_t rZ = resource(g.a, 0);
+    // copy i of an operand fills its LDS rows r = 8 i + lane / 8, slot lane % 8 with chunk slot ^ swz(r)
+    int voW[2 * NC], voA[2 * MT];
+#pragma unroll
+    for (int i = 0; i < 2 * NC; ++i) {
+        const int r = 8 * i + (lane >> 3);
+        voW[i] = (int)((n0 + r) * rowbytes + 16 * ((lane & 7) ^ chunk_swz(r)));
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+        const int r = 8 * i + (lane >> 3);
+        voA[i] = (int)((m0 + r) * rowbytes + 16 * ((lane & 7) ^ chunk_swz(r)));
+    }
+    constexpr int DPR = S::SPR / 4;  // scale dwords of a row
+    const int sp = lane % DPR;
+    int voSW[S::WSZ / 256], voSA[S::ASZ / 256];
+#pragma unroll
+    for (int i = 0; i < S::WSZ / 256; ++i) {
+        const int r = (64 * i + lane) / DPR;
+        voSW[i] = r < S::WR ? (int)((g.b_2d ? (n0 + r) >> 5 : n0 + r) * kgroups + 4 * sp) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < S::ASZ / 256; ++i) {
+        const int r = (64 * i + lane) / DPR;
+        voSA[i] = r < S::AR ? (int)((m0 + r) * kgroups + 4 * sp) : -1;
+    }
+
+    auto issue = [&](int i) {  // the wave's unit i
+        uint8_t* const st = ring + (i % D) * S::UNIT;
+        const int u = wave + NW * i;
+        const bool real = i < mine;
+        const int so = real ? u * 128 : 0, ss = real ? u * S::SPR : 0;
+        // the second half of the last unit of an E2M1 row whose K is an odd multiple of 128 is not there
+        const bool half = !FP8 && real && u * 128 + 64 >= rowbytes;
+#pragma unroll
+        for (int j = 0; j < 2 * NC; ++j) {
+            const int vo = half && (((lane & 7) ^ chunk_swz(8 * j + (lane >> 3))) >= 4) ? -1 : voW[j];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(real ? rG : rZ, (lds_ptr_t)(st + 1024 * j), 16, vo, so, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(real ? rU : rZ, (lds_ptr_t)(st + S::OFF_U + 1024 * j), 16, vo, so, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * MT; ++j) {
+            const int vo = half && (((lane & 7) ^ chunk_swz(8 * j + (lane >> 3))) >= 4) ? -1 : voA[j];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(real ? rA : rZ, (lds_ptr_t)(st + S::OFF_A + 1024 * j), 16, vo, so, 0, 0);
+        }
+        const bool gone = half && sp;
+#pragma unroll
+        for (int j = 0; j < S::WSZ / 256; ++j) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(real ? rSG : rZ, (lds_ptr_t)(st + S::OFF_SG + 256 * j), 4, gone ? -1 : voSW[j], ss, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(real ? rSU : rZ, (lds_ptr_t)(st + S::OFF_SU + 256 * j), 4, gone ? -1 : voSW[j], ss, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < S::ASZ / 256; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(real ? rSA : rZ, (lds_ptr_t)(st + S::OFF_SA + 256 * j), 4, gone ? -1 : voSA[j], ss, 0, 0);
+    };
+    const int swz = chunk_swz(fr);
+    auto frag = [&](const uint8_t* rows, int t, int j) -> v8i {  // rows 16 t + fr: (16 t + fr) swizzles like fr
+        const uint8_t* const p = rows + (16 * t + fr) * 128;
+        const u32x4 a = *reinterpret_cast<const u32x4*>(p + 16 * ((4 * j + fq) ^ swz));
+        if constexpr (FP8) {
+            const u32x4 b = *reinterpret_cast<const u32x4*>(p + 16 * ((4 + fq) ^ swz));
+            return (v8i){(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+        } else {
+            return (v8i){(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+        }
+    };
+    auto scale = [&](const uint8_t* s, int t, int j) {
+        return (int)(*reinterpret_cast<const uint32_t*>(s + (16 * t + fr) * S::SPR + 4 * j) >> (8 * fq));
+    };
+
+    f32x4 acc[2][NC][MT];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[p][c][m] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) issue(i);
+    for (int i = 0; i < mine; ++i) {
+        issue(i + D - 1);                  // into the buffer that was read last
+        wait_vm<(D - 1) * S::COPIES>();    // this wave's copies of unit i have landed
+        asm volatile("" ::: "memory");
+        const uint8_t* const st = ring + (i % D) * S::UNIT;
+#pragma unroll
+        for (int j = 0; j < S::STEPS; ++j) {
+            v8i fa[MT];
+            int sa[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                fa[m] = frag(st + S::OFF_A, m, j);
+                sa[m] = scale(st + S::OFF_SA, m, j);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const v8i fw = frag(st + p * S::OFF_U, c, j);
+                    const int sw = scale(st + (p ? S::OFF_SU : S::OFF_SG), c, j);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        acc[p][c][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fa[m], acc[p][c][m], FP8 ? 0 : 4,
+                                                                                       FP8 ? 0 : 4, 0, sw, 0, sa[m]);
+                }
+        }
+        wait_lgkm0();  // the buffer has been read
+    }
+    wait_vm<0>();  // the last copies (of nothing) have landed: the ring is free
+    __syncthreads();
+    // the shares: lane (fr, fq) holds columns 16 c + 4 fq + i of row 16 m + fr
+    float* const part = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                *reinterpret_cast<f32x4*>(part + wave * S::SHARE + (p * S::AR + 16 * m + fr) * S::HP + 16 * c + 4 * fq) = acc[p][c][m];
+    __syncthreads();
+    const int rows = (int)min((int64_t)S::AR, g.M - m0);
+    for (int i = tid; i < rows * S::WR; i += 64 * NW) {
+        const int r = i / S::WR, c = i % S::WR;
+        float gv = part[r * S::HP + c], uv = part[(S::AR + r) * S::HP + c];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) {
+            gv += part[w * S::SHARE + r * S::HP + c];
+            uv += part[w * S::SHARE + (S::AR + r) * S::HP + c];
+        }
+        const float h = act_value(gv, g.act) * uv;
+        const int64_t row = m0 + r, col = n0 + c;
+        if (col < g.N) store_gated<OUT>(g, row, col, gv, uv, h);
+        if constexpr (FQ != FQ_NONE) part[r * S::HP + c] = h;  // read by this thread alone until now
+    }
+    if constexpr (FQ != FQ_NONE) {
+        static_assert(NC == 2 && MT <= 4, "a group of 32 columns, a lane a row");
+        __syncthreads();
+        if (wave == 0) {
+            float v[32];
+            const int r = min(lane, S::AR - 1);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(part + r * S::HP + 4 * c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * c + i] = x[i];
+            }
+            quantize_group(g, v, lane < rows ? m0 + lane : g.M, n0);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------------------------
 // Few rows: 32 rows of A by 32 columns of h a workgroup of 8 waves. K is cut into units of 128 bytes of a row
 // (256 E2M1 or 128 E4M3 values); wave w takes the units w, w + 8, .. and multiplies them with 32x32x64 scaled
@@ -246,24 +461,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_gated_rows(GemmArgs g) {
             }
             hv[k] = act_value(gv, g.act) * uv;
             const int64_t row = m0 + r, col = n0 + c;
-            if (row < g.M && col < g.N) {
-                if constexpr (OUT == DT_F32) {
-                    if (g.gu) {
-                        float* d = reinterpret_cast<float*>(g.gu) + row * g.ldgu + col;
-                        d[0] = gv;
-                        d[g.N] = uv;
-                    }
-                    if (g.c) reinterpret_cast<float*>(g.c)[row * g.ldc + col] = hv[k];
-                } else {
-                    if (g.gu) {
-                        uint16_t* d = reinterpret_cast<uint16_t*>(g.gu) + row * g.ldgu + col;
-                        d[0] = (uint16_t)pack_bf16x2_rne(gv, 0.0f);
-                        d[g.N] = (uint16_t)pack_bf16x2_rne(uv, 0.0f);
-                    }
-                    if (g.c) reinterpret_cast<uint16_t*>(g.c)[row * g.ldc + col] = (uint16_t)pack_bf16x2_rne(hv[k], 0.0f);
-                }
-                if (g.h32) g.h32[row * g.N + col] = hv[k];
-            }
+            if (row < g.M && col < g.N) store_gated<OUT>(g, row, col, gv, uv, hv[k]);
         }
         if constexpr (FQ != FQ_NONE) {
             __syncthreads();
@@ -286,19 +484,49 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_gated_rows(GemmArgs g) {
 // ---------------------------------------------------------------------------------------------
 hipError_t plan_gated(int64_t M, int64_t F, int64_t K, bool fp8, const fp4_qparams* q, GatedPlan* p) {
     const int64_t rowb = fp8 ? K : K / 2;
-    const bool direct = K % (fp8 ? 128 : 256) == 0 && M * rowb < (1ll << 31) && F * rowb < (1ll << 31);
-    p->tile = 0;
-    if (direct && M > 64 && ((M + 127) / 128) * ((F + 63) / 64) <= kMaxGrid) {
+    const bool direct = M * rowb < (1ll << 31) && F * rowb < (1ll << 31);
+    int columns = 32;  // of a tile: a rotation has to lie within them
+    p->kernel = GATED_ROWS;
+    if (direct && K % 128 == 0 && M <= 64) {
+        p->kernel = GATED_STREAM;
+    } else if (direct && K % (fp8 ? 128 : 256) == 0 && ((M + 127) / 128) * ((F + 63) / 64) <= kMaxGrid) {
         int cus = 0;
         const hipError_t e = cu_count(&cus);
         if (e != hipSuccess) return e;
         const int64_t big = ((M + 255) / 256) * ((F + 127) / 128);
-        p->tile = M < 256 || F < 128 || 2 * big <= cus ? 128 : 256;
+        const bool mid = M < 256 || F < 128 || 2 * big <= cus;
+        p->kernel = mid ? GATED_TILE128 : GATED_TILE256;
+        columns = mid ? 64 : 128;
     }
-    // a rotation has to lie within a tile's columns
-    p->quant_pass = q && (q->round_mode == FP4_ROUND_SR || q->hadamard_n > (p->tile ? p->tile / 2 : 32));
+    p->quant_pass = q && (q->round_mode == FP4_ROUND_SR || q->hadamard_n > columns);
     p->ws = p->quant_pass ? M * F * 4 : 0;
     return hipSuccess;
+}
+
+template <bool FP8, int OUT, int FQ, int NC, int MT, int D>
+static hipError_t launch_stream(const GemmArgs& g, hipStream_t s) {
+    using S = Stream<FP8, NC, MT, kStreamWaves, D>;
+    const hipError_t e = allow_lds<k_gated_stream<FP8, OUT, FQ, NC, MT, kStreamWaves, D>>(S::LDS);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_gated_stream<FP8, OUT, FQ, NC, MT, kStreamWaves, D>), dim3((unsigned)((g.N + S::WR - 1) / S::WR)),
+                       dim3(64 * kStreamWaves), S::LDS, s, g);
+    return hipGetLastError();
+}
+
+template <bool FP8, int OUT, int FQ>
+static hipError_t launch_stream_m(const GemmArgs& g, hipStream_t s) {
+    // 16 columns a workgroup, so that several fit a CU and all are resident at once; 32 where groups of 32 are
+    // quantized; 48 where A's rows are most of an 8-bit unit (48 rows, K 4096, F 11008: 31.0 us, with 16 columns
+    // 32.5; in 4 bits 16.1 against 14.2)
+    constexpr int NC = FQ != FQ_NONE ? 2 : 1, NL = FQ == FQ_NONE && FP8 ? 3 : NC;
+    // two buffers where a wave has eight units or more to go through (one row, 8 bits, K 4096: 23.3 us against 24.5;
+    // 4 bits, K 8192: 18.7 against 19.3), else one, which leaves room for more workgroups (4 bits, K 4096: 9.9
+    // against 10.2)
+    const bool deep = (FP8 ? g.K / 128 : g.K / 256) >= 8 * kStreamWaves;
+    if (g.M <= 16) return deep ? launch_stream<FP8, OUT, FQ, NC, 1, 2>(g, s) : launch_stream<FP8, OUT, FQ, NC, 1, 1>(g, s);
+    if (g.M <= 32) return deep ? launch_stream<FP8, OUT, FQ, NC, 2, 2>(g, s) : launch_stream<FP8, OUT, FQ, NC, 2, 1>(g, s);
+    if (g.M <= 48) return launch_stream<FP8, OUT, FQ, NL, 3, 1>(g, s);
+    return launch_stream<FP8, OUT, FQ, NL, 4, 1>(g, s);
 }
 
 template <bool FP8, bool B2D, int OUT, int FQ, int TS>
@@ -313,9 +541,10 @@ static hipError_t launch_tile(const GemmArgs& g, hipStream_t s) {
 }
 
 template <bool FP8, bool B2D, int OUT, int FQ>
-static hipError_t launch_gated_k(const GemmArgs& g, int tile, hipStream_t s) {
-    if (tile == 256) return launch_tile<FP8, B2D, OUT, FQ, 256>(g, s);
-    if (tile == 128) return launch_tile<FP8, B2D, OUT, FQ, 128>(g, s);
+static hipError_t launch_gated_k(const GemmArgs& g, int kernel, hipStream_t s) {
+    if (kernel == GATED_TILE256) return launch_tile<FP8, B2D, OUT, FQ, 256>(g, s);
+    if (kernel == GATED_TILE128) return launch_tile<FP8, B2D, OUT, FQ, 128>(g, s);
+    if (kernel == GATED_STREAM) return launch_stream_m<FP8, OUT, FQ>(g, s);
     const int64_t tiles = ((g.N + 31) / 32) * ((g.M + 31) / 32);
     hipLaunchKernelGGL((k_gated_rows<FP8, B2D, OUT, FQ>), dim3((unsigned)(tiles < kMaxGrid ? tiles : kMaxGrid)),
                        dim3(64 * kRowsWaves), 0, s, g);
@@ -323,20 +552,20 @@ static hipError_t launch_gated_k(const GemmArgs& g, int tile, hipStream_t s) {
 }
 
 template <int OUT, int FQ>
-static hipError_t launch_gated_q(const GemmArgs& g, int kind, int tile, hipStream_t s) {
-    if (kind == 1) return launch_gated_k<true, false, OUT, FQ>(g, tile, s);
-    return g.b_2d ? launch_gated_k<false, true, OUT, FQ>(g, tile, s) : launch_gated_k<false, false, OUT, FQ>(g, tile, s);
+static hipError_t launch_gated_q(const GemmArgs& g, int kind, int kernel, hipStream_t s) {
+    if (kind == 1) return launch_gated_k<true, false, OUT, FQ>(g, kernel, s);
+    return g.b_2d ? launch_gated_k<false, true, OUT, FQ>(g, kernel, s) : launch_gated_k<false, false, OUT, FQ>(g, kernel, s);
 }
 
 template <int OUT>
-static hipError_t launch_gated_o(const GemmArgs& g, int kind, int tile, int fused_q, hipStream_t s) {
-    return fused_q ? launch_gated_q<OUT, FQ_RNE>(g, kind, tile, s) : launch_gated_q<OUT, FQ_NONE>(g, kind, tile, s);
+static hipError_t launch_gated_o(const GemmArgs& g, int kind, int kernel, int fused_q, hipStream_t s) {
+    return fused_q ? launch_gated_q<OUT, FQ_RNE>(g, kind, kernel, s) : launch_gated_q<OUT, FQ_NONE>(g, kind, kernel, s);
 }
 
 hipError_t launch_gated(GemmArgs g, const GatedPlan& p, int kind, int dtype, int fused_q, void* ws, hipStream_t s) {
     g.h32 = p.quant_pass ? reinterpret_cast<float*>(ws) : nullptr;
     const int fused = fused_q && !p.quant_pass;
-    const hipError_t e = dtype == DT_BF16 ? launch_gated_o<DT_BF16>(g, kind, p.tile, fused, s) : launch_gated_o<DT_F32>(g, kind, p.tile, fused, s);
+    const hipError_t e = dtype == DT_BF16 ? launch_gated_o<DT_BF16>(g, kind, p.kernel, fused, s) : launch_gated_o<DT_F32>(g, kind, p.kernel, fused, s);
     if (e != hipSuccess || !p.quant_pass) return e;
     SegArgs a{};
     a.x = ws;

@@ -71,8 +71,9 @@ struct RopeArgs {
 hipError_t launch_rope(const RopeArgs& a, int dtype, int layout, hipStream_t s);
 
 // How a gated product is carried out: the same for the size query and the launch.
+enum { GATED_ROWS = 0, GATED_STREAM, GATED_TILE128, GATED_TILE256 };
 struct GatedPlan {
-    int tile;       // 0: few rows, else the rows of a tile
+    int kernel;     // GATED_*
     int quant_pass; // h goes to the workspace in fp32 and is quantized by a pass of its own
     int64_t ws;
 };
