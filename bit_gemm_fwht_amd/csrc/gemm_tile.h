@@ -1,12 +1,11 @@
 // The pipelined tile of the block-scaled GEMM (256 x 256 or 128 x 128 results a workgroup, operands copied
 // straight into LDS, scaled matrix instructions) with its epilogue, shared by the GEMM kernels and the gated
-// feed-forward, and what their launchers share.
+// feed-forward.
 #pragma once
-
-#include <atomic>
 
 #include "device.h"
 #include "fp4_internal.h"
+#include "launch.h"
 #include "quant_block.h"
 
 namespace bgf {
@@ -588,32 +587,6 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint
 
     if constexpr (GATED) gated_epilogue<FP8, OUT, FQ, TS>(g, acc, m0, n0, smem);
     else big_epilogue<FP8, OUT, NVG, FQ, TS>(g, acc, m0, n0, smem);
-}
-
-// Raises KERNEL's dynamic LDS limit to `lds` bytes once per device (the attribute belongs to the
-// function on the current device), instead of on every launch.
-template <auto KERNEL>
-static hipError_t allow_lds(size_t lds) {
-    static std::atomic<uint64_t> done{0};  // bit d: set on device d
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    if (dev < 64 && ((done.load(std::memory_order_acquire) >> dev) & 1u)) return hipSuccess;
-    e = hipFuncSetAttribute((const void*)KERNEL, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e == hipSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_acq_rel);
-    return e;
-}
-
-// Compute units of the current device (looked up once per device).
-inline hipError_t cu_count(int* n) {
-    static std::atomic<int> cus[64];
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    if (dev < 64 && (*n = cus[dev].load(std::memory_order_acquire)) > 0) return hipSuccess;
-    e = hipDeviceGetAttribute(n, hipDeviceAttributeMultiprocessorCount, dev);
-    if (e == hipSuccess && dev < 64) cus[dev].store(*n, std::memory_order_release);
-    return e;
 }
 
 }  // namespace bgf

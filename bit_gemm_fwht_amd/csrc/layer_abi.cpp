@@ -170,7 +170,7 @@ int fp4_rmsnorm(const fp4_norm* n, const fp4_qparams* out_q, fp4_qtensor* y_q, v
         a.lds = n->lds;
         a.ldy = n->ldy;
         a.cols = (int)n->cols;
-        a.w_bf16 = n->w_dtype == FP4_DT_BF16;
+        a.w_kind = !n->weight ? W_NONE : n->w_dtype == FP4_DT_BF16 ? W_BF16 : W_F32;
         a.eps = n->eps;
         set_quant(y_q, out_q, n->rows, n->cols);
         return hip_status(launch_rmsnorm(a, n->dtype, rnd_of(out_q), reinterpret_cast<hipStream_t>(stream)));
@@ -228,7 +228,7 @@ int fp4_rmsnorm_backward(const fp4_norm_grad* n, void* workspace, int64_t ws_byt
         a.lddsum = n->lddsum;
         a.lddx = n->lddx;
         a.cols = (int)n->cols;
-        a.w_bf16 = n->w_dtype == FP4_DT_BF16;
+        a.w_kind = !n->weight ? W_NONE : n->w_dtype == FP4_DT_BF16 ? W_BF16 : W_F32;
         a.eps = n->eps;
         return hip_status(launch_rmsnorm_grad(a, p, n->dtype, reinterpret_cast<hipStream_t>(stream)));
     } catch (...) {

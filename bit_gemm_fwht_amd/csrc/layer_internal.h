@@ -21,6 +21,8 @@ struct QuantOut {
     int elem, ceil_rule, hn;
 };
 
+enum { W_NONE = 0, W_BF16, W_F32 };  // how a norm's weight is stored; none: ones
+
 struct NormArgs {
     const void* x;
     const void* r;
@@ -28,7 +30,7 @@ struct NormArgs {
     void* sum;
     void* y;
     int64_t rows, ldx, ldr, lds, ldy;
-    int cols, w_bf16;
+    int cols, w_kind;  // w_kind: W_*
     float eps;
     QuantOut q;
 };
@@ -43,7 +45,7 @@ struct NormGradArgs {
     float* dw;
     float* part;  // [slots, cols]: partial sums of dw
     int64_t rows, lddy, lds, lddsum, lddx;
-    int cols, w_bf16;
+    int cols, w_kind;  // w_kind: W_*
     float eps;
 };
 // How the rows are dealt: the same for the size query and the launch.

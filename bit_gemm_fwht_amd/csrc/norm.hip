@@ -4,6 +4,7 @@
 // elements (piece.h) stay in registers between the sum of squares and the output, so x and r are read once
 // and s, y and the codes written once.
 #include "device.h"
+#include "launch.h"
 #include "layer_internal.h"
 #include "piece.h"
 
@@ -12,7 +13,8 @@ namespace bgf {
 constexpr int kNormThreads = 512;  // of a workgroup at most: rows of 32768 in 8 pieces a lane
 
 // Sums of a and b over the `lanes` lanes of a row (a power of two; above 64 the whole workgroup), in a fixed
-// order. red: 2 floats a wave; every thread of the workgroup calls it.
+// order. red: 2 floats a wave, another set for each of two calls that follow one another; every thread of the
+// workgroup calls it.
 __device__ __forceinline__ void row_sums(float& a, float& b, int lanes, float* red) {
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
@@ -23,7 +25,6 @@ __device__ __forceinline__ void row_sums(float& a, float& b, int lanes, float* r
     }
     if (lanes > 64) {
         const int nw = blockDim.x >> 6, wave = threadIdx.x >> 6;
-        __syncthreads();  // the last row's sums have been read
         if ((threadIdx.x & 63) == 0) {
             red[2 * wave] = a;
             red[2 * wave + 1] = b;
@@ -38,32 +39,66 @@ __device__ __forceinline__ void row_sums(float& a, float& b, int lanes, float* r
     }
 }
 
-template <int IN, int NP, int FQ>
+// A piece of the weight as it is stored, and its values.
+__device__ __forceinline__ void weight_load(Piece<DT_F32>& t, const void* w, int kind, int p) {
+    if (kind == W_BF16) {
+        Piece<DT_BF16> h;
+        piece_load<DT_BF16>(h, w, 8 * p);
+        t.w[0] = h.w[0];
+    } else if (kind == W_F32) {
+        piece_load<DT_F32>(t, w, 8 * p);
+    }
+}
+__device__ __forceinline__ void weight_values(const Piece<DT_F32>& t, int kind, float (&v)[8]) {
+    if (kind == W_BF16) {
+        Piece<DT_BF16> h;
+        h.w[0] = t.w[0];
+        piece_values<DT_BF16>(h, v);
+    } else if (kind == W_F32) {
+        piece_values<DT_F32>(t, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 1.0f;
+    }
+}
+
+// Loads are unconditional: lanes past the row's end or the last row read the last piece or row again, whose
+// values count for nothing (a load behind a condition waits for the ones before it).
+template <int IN, int NP, int FQ, bool RES, bool NT>
 __global__ __launch_bounds__(kNormThreads) void k_rmsnorm(NormArgs a, int lanes) {
-    __shared__ float red[2 * kNormThreads / 64];
-    const int at = threadIdx.x & (lanes - 1), per = blockDim.x / lanes, sub = threadIdx.x / lanes;
+    __shared__ float red[2][2 * kNormThreads / 64];
+    const int per = blockDim.x / lanes, sub = threadIdx.x / lanes, at = threadIdx.x - sub * lanes;
     const int pieces = a.cols >> 3;
     const float inv_cols = 1.0f / (float)a.cols;
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.rows; r0 += (int64_t)gridDim.x * per) {
-        const int64_t row = r0 + sub;
-        const bool in = row < a.rows;
-        Piece<IN> x[NP], r[NP];
+    Piece<IN> x[NP], r[NP];
+    auto load = [&](int64_t r0) {
+        const int64_t row = min(r0 + sub, a.rows - 1);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int p = at + lanes * i;
-            piece_zero<IN>(x[i]);
-            piece_zero<IN>(r[i]);
-            if (in && p < pieces) {
-                piece_load<IN>(x[i], a.x, row * a.ldx + 8 * p);
-                if (a.r) piece_load<IN>(r[i], a.r, row * a.ldr + 8 * p);
-            }
+            const int p = min(at + lanes * i, pieces - 1);
+            piece_load<IN, NT>(x[i], a.x, row * a.ldx + 8 * p);
+            if constexpr (RES) piece_load<IN, NT>(r[i], a.r, row * a.ldr + 8 * p);
         }
+    };
+    load((int64_t)blockIdx.x * per);
+    // the weight stays in registers where there is room beside the next row, else it is read again for each row
+    constexpr bool KEPT = NP <= 2;
+    Piece<DT_F32> w[NP];
+    auto load_weight = [&]() {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) weight_load(w[i], a.w, a.w_kind, min(at + lanes * i, pieces - 1));
+    };
+    if constexpr (KEPT) load_weight();
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.rows; r0 += (int64_t)gridDim.x * per, turn ^= 1) {
+        const int64_t row = r0 + sub;
+        const bool in = row < a.rows;
         float v[NP][8], ss = 0.0f, none = 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int p = at + lanes * i;
             piece_values<IN>(x[i], v[i]);
-            if (a.r) {
+            if constexpr (RES) {
                 float rv[8];
                 piece_values<IN>(r[i], rv);
 #pragma unroll
@@ -72,31 +107,26 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm(NormArgs a, int lanes)
                 piece_values<IN>(s, v[i]);  // what the sum holds is what is normed
                 if (in && p < pieces) piece_store<IN>(a.sum, row * a.lds + 8 * p, s);
             }
+            if (p >= pieces) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[i][j], v[i][j], ss);
         }
-        row_sums(ss, none, lanes, red);
+        // the weight first: loads return in order; then the next row, on its way during this one's sums and codes
+        if constexpr (!KEPT) load_weight();
+        load(r0 + (int64_t)gridDim.x * per);
+        row_sums(ss, none, lanes, red[turn]);
         const float rstd = 1.0f / sqrtf(ss * inv_cols + a.eps);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int p = at + lanes * i;
             const bool here = in && p < pieces;
-            float w[8];
+            float wv[8];
+            weight_values(w[i], a.w_kind, wv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-            if (a.w && here) {
-                if (a.w_bf16) {
-                    Piece<DT_BF16> t;
-                    piece_load<DT_BF16>(t, a.w, 8 * p);
-                    piece_values<DT_BF16>(t, w);
-                } else {
-                    Piece<DT_F32> t;
-                    piece_load<DT_F32>(t, a.w, 8 * p);
-                    piece_values<DT_F32>(t, w);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
+            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * wv[j];
             if (a.y && here) piece_store<IN>(a.y, row * a.ldy + 8 * p, piece_pack<IN>(v[i]));
             // every lane takes part: a group's and a chunk's lanes exchange values
             if constexpr (FQ != 0)
@@ -112,19 +142,62 @@ static int row_lanes(int cols, int most) {
     return lanes;
 }
 
+// How a row's pieces are dealt: the lanes of a row and the pieces of a lane. Up to 64 pieces: a part of a wave, a
+// power of two of lanes, one piece each. Above: one row a workgroup of 1, 2, 4 or 8 waves (5 on 4 SIMDs: 6000 rows of
+// 5120 in 68.5 us, 4 waves with 3 pieces a lane 53.6), so that few lanes are idle, and then with 2 pieces a lane, which
+// keep more of a row in flight (8192 rows of 4096: 52.6 us, with 1 piece 59.9, with 4 59.4), or 1 where all rows
+// are resident at once and a row's latency counts (one row of 4096: 4.0 us against 5.1).
+struct RowPlan {
+    int lanes, np;
+};
+static RowPlan plan_row(int cols, bool few) {
+    const int pieces = cols / 8;
+    RowPlan best{8, 1};
+    if (pieces <= 64) {
+        while (best.lanes < pieces) best.lanes *= 2;
+        return best;
+    }
+    const int nps[] = {few ? 1 : 2, few ? 2 : 1, 3, 4, 6, 8};
+    int idle = 1 << 30;
+    for (int np : nps)
+        for (int lanes = 64; lanes <= kNormThreads; lanes *= 2)
+            if (lanes * np >= pieces && lanes * np - pieces < idle) {
+                idle = lanes * np - pieces;
+                best = RowPlan{lanes, np};
+            }
+    return best;
+}
+
+template <int IN, int FQ, bool RES, bool NT>
+static hipError_t launch_rmsnorm_r(const NormArgs& a, hipStream_t s) {
+    int cus = 0;
+    const hipError_t e = cu_count(&cus);
+    if (e != hipSuccess) return e;
+    const bool few = a.rows <= 4 * cus;
+    const RowPlan r = plan_row(a.cols, few);
+    const int threads = r.lanes > 64 ? r.lanes : 256, per = threads / r.lanes;
+    // few rows: a workgroup each; else 1024 threads a CU, which go through several rows with the next one on its way
+    // (8192 rows of 4096: 49.6 us, with 2048 threads a CU 51.9, a workgroup for each row 54.2)
+    const int64_t need = (a.rows + per - 1) / per, most = few ? need : (int64_t)cus * (1024 / threads);
+    const dim3 grid((unsigned)(need < most ? need : most)), block(threads);
+    if (r.np == 1) hipLaunchKernelGGL((k_rmsnorm<IN, 1, FQ, RES, NT>), grid, block, 0, s, a, r.lanes);
+    else if (r.np == 2) hipLaunchKernelGGL((k_rmsnorm<IN, 2, FQ, RES, NT>), grid, block, 0, s, a, r.lanes);
+    else if (r.np == 3) hipLaunchKernelGGL((k_rmsnorm<IN, 3, FQ, RES, NT>), grid, block, 0, s, a, r.lanes);
+    else if (r.np == 4) hipLaunchKernelGGL((k_rmsnorm<IN, 4, FQ, RES, NT>), grid, block, 0, s, a, r.lanes);
+    else if (r.np == 6) hipLaunchKernelGGL((k_rmsnorm<IN, 6, FQ, RES, NT>), grid, block, 0, s, a, r.lanes);
+    else hipLaunchKernelGGL((k_rmsnorm<IN, 8, FQ, RES, NT>), grid, block, 0, s, a, r.lanes);
+    return hipGetLastError();
+}
+
 template <int IN, int FQ>
 static hipError_t launch_rmsnorm_k(const NormArgs& a, hipStream_t s) {
-    const int pieces = (a.cols + 7) / 8;
-    const int lanes = row_lanes(a.cols, kNormThreads);
-    const int threads = lanes > 64 ? lanes : 256, per = threads / lanes;  // above a wave: one row a workgroup
-    const int64_t need = (a.rows + per - 1) / per;
-    const unsigned grid = (unsigned)(need < kMaxGrid ? need : kMaxGrid);
-    const int np = (pieces + lanes - 1) / lanes;
-    if (np <= 1) hipLaunchKernelGGL((k_rmsnorm<IN, 1, FQ>), dim3(grid), dim3(threads), 0, s, a, lanes);
-    else if (np <= 2) hipLaunchKernelGGL((k_rmsnorm<IN, 2, FQ>), dim3(grid), dim3(threads), 0, s, a, lanes);
-    else if (np <= 4) hipLaunchKernelGGL((k_rmsnorm<IN, 4, FQ>), dim3(grid), dim3(threads), 0, s, a, lanes);
-    else hipLaunchKernelGGL((k_rmsnorm<IN, 8, FQ>), dim3(grid), dim3(threads), 0, s, a, lanes);
-    return hipGetLastError();
+    // bf16 that is more than the caches keep is not kept there (128 MiB read: 52.6 us, kept 54.4; 64 MiB: kept 35.1,
+    // not kept 38.4). fp32 always is: a lane's two 16-byte halves touch the same cache line one after the other.
+    if constexpr (IN == DT_BF16) {
+        if (a.rows * a.cols * (a.r ? 4 : 2) >= (int64_t(96) << 20))
+            return a.r ? launch_rmsnorm_r<IN, FQ, true, true>(a, s) : launch_rmsnorm_r<IN, FQ, false, true>(a, s);
+    }
+    return a.r ? launch_rmsnorm_r<IN, FQ, true, false>(a, s) : launch_rmsnorm_r<IN, FQ, false, false>(a, s);
 }
 
 hipError_t launch_rmsnorm(const NormArgs& a, int dtype, int rnd, hipStream_t s) {
@@ -142,8 +215,8 @@ hipError_t launch_rmsnorm(const NormArgs& a, int dtype, int rnd, hipStream_t s) 
 // ---------------------------------------------------------------------------------------------
 template <int IN, int NP>
 __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, int lanes) {
-    __shared__ float red[2 * kNormThreads / 64];
-    const int at = threadIdx.x & (lanes - 1), per = blockDim.x / lanes, sub = threadIdx.x / lanes;
+    __shared__ float red[2][2 * kNormThreads / 64];
+    const int per = blockDim.x / lanes, sub = threadIdx.x / lanes, at = threadIdx.x - sub * lanes;
     const int pieces = a.cols >> 3;
     const float inv_cols = 1.0f / (float)a.cols;
     float dw[NP][8], w[NP][8];
@@ -151,23 +224,13 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
     for (int i = 0; i < NP; ++i) {
         const int p = at + lanes * i;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            dw[i][j] = 0.0f;
-            w[i][j] = 1.0f;
-        }
-        if (a.w && p < pieces) {
-            if (a.w_bf16) {
-                Piece<DT_BF16> t;
-                piece_load<DT_BF16>(t, a.w, 8 * p);
-                piece_values<DT_BF16>(t, w[i]);
-            } else {
-                Piece<DT_F32> t;
-                piece_load<DT_F32>(t, a.w, 8 * p);
-                piece_values<DT_F32>(t, w[i]);
-            }
-        }
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+        Piece<DT_F32> t;
+        weight_load(t, a.w, a.w_kind, min(p, pieces - 1));
+        weight_values(t, a.w_kind, w[i]);
     }
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.rows; r0 += (int64_t)gridDim.x * per) {
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.rows; r0 += (int64_t)gridDim.x * per, turn ^= 1) {
         const int64_t row = r0 + sub;
         const bool in = row < a.rows;
         Piece<IN> s[NP], dy[NP], ds[NP];
@@ -195,7 +258,7 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
                 as = __builtin_fmaf(dv[j] * w[i][j], sv[j], as);
             }
         }
-        row_sums(ss, as, lanes, red);
+        row_sums(ss, as, lanes, red[turn]);
         const float rstd = 1.0f / sqrtf(ss * inv_cols + a.eps);
         const float c = as * inv_cols * rstd * rstd;  // mean(a n) r: dx = r (a - s c) + dsum
 #pragma unroll

@@ -18,11 +18,12 @@ struct Piece {
     u32x4 w[N];
 };
 
-template <int DT>
+// NT: read once, not to be kept in the caches
+template <int DT, bool NT = false>
 __device__ __forceinline__ void piece_load(Piece<DT>& p, const void* base, int64_t elem) {
     const u32x4* s = reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(base) + elem * (DT == DT_BF16 ? 2 : 4));
 #pragma unroll
-    for (int i = 0; i < Piece<DT>::N; ++i) p.w[i] = s[i];
+    for (int i = 0; i < Piece<DT>::N; ++i) p.w[i] = NT ? __builtin_nontemporal_load(s + i) : s[i];
 }
 
 template <int DT>
