@@ -51,6 +51,7 @@ struct NormGradArgs {
 // How the rows are dealt: the same for the size query and the launch.
 struct NormGradPlan {
     int lanes;    // lanes of a row
+    int np;       // pieces of a lane
     int threads;  // of a workgroup
     int grid;
     int slots;    // partial sums of dw, 0: no dw

@@ -135,13 +135,6 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm(NormArgs a, int lanes)
     }
 }
 
-// lanes of a row: a power of two that covers its pieces, at most `most`
-static int row_lanes(int cols, int most) {
-    int lanes = 8;
-    while (lanes < most && lanes < cols / 8) lanes *= 2;
-    return lanes;
-}
-
 // How a row's pieces are dealt: the lanes of a row and the pieces of a lane. Up to 64 pieces: a part of a wave, a
 // power of two of lanes, one piece each. Above: one row a workgroup of 1, 2, 4 or 8 waves (5 on 4 SIMDs: 6000 rows of
 // 5120 in 68.5 us, 4 waves with 3 pieces a lane 53.6), so that few lanes are idle, and then with 2 pieces a lane, which
@@ -213,50 +206,66 @@ hipError_t launch_rmsnorm(const NormArgs& a, int dtype, int rnd, hipStream_t s) 
 // Both means come from one pass over the row (sum s^2 and sum a s, then mean(a n) = r sum(a s) / cols). A
 // workgroup keeps its rows' part of dw in registers and writes it once; k_sum_slots adds the parts.
 // ---------------------------------------------------------------------------------------------
-template <int IN, int NP>
+template <int IN, int NP, bool NT>
 __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, int lanes) {
     __shared__ float red[2][2 * kNormThreads / 64];
     const int per = blockDim.x / lanes, sub = threadIdx.x / lanes, at = threadIdx.x - sub * lanes;
     const int pieces = a.cols >> 3;
     const float inv_cols = 1.0f / (float)a.cols;
-    float dw[NP][8], w[NP][8];
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const int p = at + lanes * i;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-        Piece<DT_F32> t;
-        weight_load(t, a.w, a.w_kind, min(p, pieces - 1));
-        weight_values(t, a.w_kind, w[i]);
-    }
-    int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.rows; r0 += (int64_t)gridDim.x * per, turn ^= 1) {
-        const int64_t row = r0 + sub;
-        const bool in = row < a.rows;
+    struct Row {
         Piece<IN> s[NP], dy[NP], ds[NP];
+    };
+    auto load = [&](Row& t, int64_t r0) {  // without conditions, as in the forward pass
+        const int64_t row = min(r0 + sub, a.rows - 1);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int p = at + lanes * i;
-            piece_zero<IN>(s[i]);
-            piece_zero<IN>(dy[i]);
-            piece_zero<IN>(ds[i]);
-            if (in && p < pieces) {
-                piece_load<IN>(s[i], a.s, row * a.lds + 8 * p);
-                piece_load<IN>(dy[i], a.dy, row * a.lddy + 8 * p);
-                if (a.dsum) piece_load<IN>(ds[i], a.dsum, row * a.lddsum + 8 * p);
-            }
+            const int p = min(at + lanes * i, pieces - 1);
+            piece_load<IN, NT>(t.s[i], a.s, row * a.lds + 8 * p);
+            piece_load<IN, NT>(t.dy[i], a.dy, row * a.lddy + 8 * p);
+            if (a.dsum) piece_load<IN, NT>(t.ds[i], a.dsum, row * a.lddsum + 8 * p);
+            else piece_zero<IN>(t.ds[i]);
+        }
+    };
+    // the next row is loaded during the present one where both fit the registers
+    constexpr bool AHEAD = NP * (IN == DT_BF16 ? 1 : 2) <= 3;
+    const int64_t step = (int64_t)gridDim.x * per;
+    Row next;
+    if constexpr (AHEAD) load(next, (int64_t)blockIdx.x * per);
+    float dw[NP][8];
+    Piece<DT_F32> w[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        weight_load(w[i], a.w, a.w_kind, min(at + lanes * i, pieces - 1));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    }
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.rows; r0 += step, turn ^= 1) {
+        const int64_t row = r0 + sub;
+        const bool in = row < a.rows;
+        Row t;
+        if constexpr (AHEAD) {
+            t = next;
+            load(next, r0 + step);
+        } else {
+            load(t, r0);
         }
         float ss = 0.0f, as = 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            float sv[8], dv[8];
-            piece_values<IN>(s[i], sv);
-            piece_values<IN>(dy[i], dv);
+            const bool here = in && at + lanes * i < pieces;
+            float sv[8], dv[8], wv[8];
+            piece_values<IN>(t.s[i], sv);
+            piece_values<IN>(t.dy[i], dv);
+            weight_values(w[i], a.w_kind, wv);
+            float q = 0.0f, d = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                ss = __builtin_fmaf(sv[j], sv[j], ss);
-                as = __builtin_fmaf(dv[j] * w[i][j], sv[j], as);
+                q = __builtin_fmaf(sv[j], sv[j], q);
+                d = __builtin_fmaf(dv[j] * wv[j], sv[j], d);
             }
+            ss += here ? q : 0.0f;
+            as += here ? d : 0.0f;
         }
         row_sums(ss, as, lanes, red[turn]);
         const float rstd = 1.0f / sqrtf(ss * inv_cols + a.eps);
@@ -264,16 +273,19 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int p = at + lanes * i;
-            float sv[8], dv[8], o[8], base[8];
-            piece_values<IN>(s[i], sv);
-            piece_values<IN>(dy[i], dv);
-            piece_values<IN>(ds[i], base);
+            const bool here = in && p < pieces;
+            float sv[8], dv[8], wv[8], o[8], base[8];
+            piece_values<IN>(t.s[i], sv);
+            piece_values<IN>(t.dy[i], dv);
+            piece_values<IN>(t.ds[i], base);
+            weight_values(w[i], a.w_kind, wv);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                o[j] = __builtin_fmaf(rstd, dv[j] * w[i][j] - sv[j] * c, base[j]);
-                dw[i][j] = __builtin_fmaf(dv[j], sv[j] * rstd, dw[i][j]);
+                o[j] = __builtin_fmaf(rstd, dv[j] * wv[j] - sv[j] * c, base[j]);
+                // (a row that is not there was read as another one)
+                dw[i][j] = __builtin_fmaf(in ? dv[j] : 0.0f, sv[j] * rstd, dw[i][j]);
             }
-            if (in && p < pieces) piece_store<IN>(a.dx, row * a.lddx + 8 * p, piece_pack<IN>(o));
+            if (here) piece_store<IN>(a.dx, row * a.lddx + 8 * p, piece_pack<IN>(o));
         }
     }
     if (!a.part) return;
@@ -294,54 +306,66 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
     }
 }
 
-// dw[c] = sum of part[slot][c], slots in order within each of 64 runs, then the runs in order: 16 columns by 64 runs
-// a workgroup.
+// dw[c] = sum of part[slot][c] in a fixed order: 32 columns a workgroup, 4 a thread, the slots in 128 runs, then
+// the runs by fours, then those 32.
 __global__ __launch_bounds__(1024) void k_sum_slots(const float* part, int slots, int cols, float* dw) {
-    __shared__ float run[64][17];
-    const int c = blockIdx.x * 16 + (threadIdx.x & 15), g = threadIdx.x >> 4;
-    const int each = (slots + 63) / 64, s0 = g * each, s1 = min(slots, s0 + each);
-    float t = 0.0f;
+    __shared__ float run[128][33], four[32][33];
+    const int k = threadIdx.x & 7, g = threadIdx.x >> 3, c = blockIdx.x * 32 + 4 * k;
+    const int each = (slots + 127) / 128, s0 = g * each, s1 = min(slots, s0 + each);
+    f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < cols)
-        for (int s = s0; s < s1; ++s) t += part[(int64_t)s * cols + c];
-    run[g][threadIdx.x & 15] = t;
+        for (int s = s0; s < s1; ++s) t += *reinterpret_cast<const f32x4*>(part + (int64_t)s * cols + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) run[g][4 * k + i] = t[i];
     __syncthreads();
-    if (g == 0 && c < cols) {
-        for (int i = 1; i < 64; ++i) t += run[i][threadIdx.x];
-        dw[c] = t;
+    const int col = threadIdx.x & 31, q = threadIdx.x >> 5;
+    four[q][col] = (run[4 * q][col] + run[4 * q + 1][col]) + (run[4 * q + 2][col] + run[4 * q + 3][col]);
+    __syncthreads();
+    if (q == 0 && blockIdx.x * 32 + col < cols) {
+        float v = four[0][col];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) v += four[i][col];
+        dw[blockIdx.x * 32 + col] = v;
     }
 }
 
+// 512 threads a CU (of 256): each carries its part of dw through many rows, so that the parts, which are written and
+// read again, stay few (8192 rows of 4096: 52.7 us; with 1024 threads a CU 59.2, with 1 piece a lane 60.9).
 NormGradPlan plan_rmsnorm_grad(int64_t rows, int cols, bool dw) {
     NormGradPlan p;
-    p.lanes = row_lanes(cols, kNormThreads);
+    const RowPlan r = plan_row(cols, rows <= 1024);
+    p.lanes = r.lanes;
+    p.np = r.np;
     p.threads = p.lanes > 64 ? p.lanes : 256;
     const int per = p.threads / p.lanes;
-    const int64_t need = (rows + per - 1) / per, most = 512;
+    const int64_t need = (rows + per - 1) / per, most = 256 * (512 / p.threads);
     p.grid = (int)(need < most ? need : most);
     p.slots = dw ? (p.lanes > 64 ? p.grid : p.grid * (p.threads / 64)) : 0;
     return p;
 }
 
+template <int IN, bool NT>
+static hipError_t launch_rmsnorm_grad_k(const NormGradArgs& a, const NormGradPlan& p, hipStream_t s) {
+    const dim3 g(p.grid), t(p.threads);
+    if (p.np == 1) hipLaunchKernelGGL((k_rmsnorm_grad<IN, 1, NT>), g, t, 0, s, a, p.lanes);
+    else if (p.np == 2) hipLaunchKernelGGL((k_rmsnorm_grad<IN, 2, NT>), g, t, 0, s, a, p.lanes);
+    else if (p.np == 3) hipLaunchKernelGGL((k_rmsnorm_grad<IN, 3, NT>), g, t, 0, s, a, p.lanes);
+    else if (p.np == 4) hipLaunchKernelGGL((k_rmsnorm_grad<IN, 4, NT>), g, t, 0, s, a, p.lanes);
+    else if (p.np == 6) hipLaunchKernelGGL((k_rmsnorm_grad<IN, 6, NT>), g, t, 0, s, a, p.lanes);
+    else hipLaunchKernelGGL((k_rmsnorm_grad<IN, 8, NT>), g, t, 0, s, a, p.lanes);
+    return hipGetLastError();
+}
+
 hipError_t launch_rmsnorm_grad(const NormGradArgs& a, const NormGradPlan& p, int dtype, hipStream_t s) {
     if (p.grid > 0) {
-        const int np = ((a.cols + 7) / 8 + p.lanes - 1) / p.lanes;
-        const dim3 g(p.grid), t(p.threads);
-        if (dtype == DT_BF16) {
-            if (np <= 1) hipLaunchKernelGGL((k_rmsnorm_grad<DT_BF16, 1>), g, t, 0, s, a, p.lanes);
-            else if (np <= 2) hipLaunchKernelGGL((k_rmsnorm_grad<DT_BF16, 2>), g, t, 0, s, a, p.lanes);
-            else if (np <= 4) hipLaunchKernelGGL((k_rmsnorm_grad<DT_BF16, 4>), g, t, 0, s, a, p.lanes);
-            else hipLaunchKernelGGL((k_rmsnorm_grad<DT_BF16, 8>), g, t, 0, s, a, p.lanes);
-        } else {
-            if (np <= 1) hipLaunchKernelGGL((k_rmsnorm_grad<DT_F32, 1>), g, t, 0, s, a, p.lanes);
-            else if (np <= 2) hipLaunchKernelGGL((k_rmsnorm_grad<DT_F32, 2>), g, t, 0, s, a, p.lanes);
-            else if (np <= 4) hipLaunchKernelGGL((k_rmsnorm_grad<DT_F32, 4>), g, t, 0, s, a, p.lanes);
-            else hipLaunchKernelGGL((k_rmsnorm_grad<DT_F32, 8>), g, t, 0, s, a, p.lanes);
-        }
-        const hipError_t e = hipGetLastError();
+        const bool nt = a.rows * a.cols * (a.dsum ? 6 : 4) >= (int64_t(96) << 20);  // as in the forward pass
+        const hipError_t e = dtype == DT_F32 ? launch_rmsnorm_grad_k<DT_F32, false>(a, p, s)
+                             : nt            ? launch_rmsnorm_grad_k<DT_BF16, true>(a, p, s)
+                                             : launch_rmsnorm_grad_k<DT_BF16, false>(a, p, s);
         if (e != hipSuccess) return e;
     }
     if (!a.dw) return hipSuccess;
-    hipLaunchKernelGGL(k_sum_slots, dim3((a.cols + 15) / 16), dim3(1024), 0, s, a.part, p.slots, a.cols, a.dw);
+    hipLaunchKernelGGL(k_sum_slots, dim3((a.cols + 31) / 32), dim3(1024), 0, s, a.part, p.slots, a.cols, a.dw);
     return hipGetLastError();
 }
 
