@@ -16,24 +16,27 @@
 
 namespace bgf {
 
-// Store a staged fp32 tile [ROWS][COLS] (row pitch `pitch` bytes in LDS) as dtype OUT at c[m0 ..][n0 ..],
-// 16-byte pieces where the place allows; rows from M and columns from N on are not there.
-template <int OUT, int ROWS, int COLS, int NTH>
+// Store a staged tile [ROWS][COLS] of dtype OUT (SRC: as it is staged, OUT or fp32; row pitch `pitch` bytes in LDS)
+// at c[m0 ..][n0 ..], 16-byte pieces where the place allows; rows from M and columns from N on are not there. A
+// thread keeps its piece of the columns and walks down the rows.
+template <int OUT, int SRC, int ROWS, int COLS, int NTH>
 __device__ __forceinline__ void store_staged(const uint8_t* lds, int pitch, char* c, int64_t ldc, int64_t m0, int64_t n0,
                                              int64_t M, int64_t N) {
     constexpr int ESZ = OUT == DT_F32 ? 4 : 2, EPC = 16 / ESZ, PPR = COLS / EPC;
+    static_assert(NTH % PPR == 0, "whole rows a sweep");
     const bool vec_ok = ((reinterpret_cast<uintptr_t>(c) & 15) == 0) && ((ldc * ESZ) % 16 == 0);
-#pragma unroll 2
-    for (int t = threadIdx.x; t < ROWS * PPR; t += NTH) {
-        const int r = t / PPR, k = (t % PPR) * EPC;
-        const int64_t m = m0 + r, n = n0 + k;
+    const int k = ((int)threadIdx.x % PPR) * EPC;
+    const int64_t n = n0 + k;
+#pragma unroll 4
+    for (int r = threadIdx.x / PPR; r < ROWS; r += NTH / PPR) {
+        const int64_t m = m0 + r;
         if (m >= M) break;
-        const float* src = reinterpret_cast<const float*>(lds + r * pitch) + k;
+        const uint8_t* src = lds + r * pitch + k * (SRC == DT_F32 ? 4 : 2);
         u32x4 val;
-        if constexpr (OUT == DT_F32) {
+        if constexpr (SRC == OUT) {
             val = *reinterpret_cast<const u32x4*>(src);
         } else {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 4);
+            const f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 16);
             val = (u32x4){pack_bf16x2_rne(a[0], a[1]), pack_bf16x2_rne(a[2], a[3]), pack_bf16x2_rne(b[0], b[1]),
                           pack_bf16x2_rne(b[2], b[3])};
         }
@@ -41,6 +44,7 @@ __device__ __forceinline__ void store_staged(const uint8_t* lds, int pitch, char
         if (vec_ok && n + EPC <= N) {
             *reinterpret_cast<u32x4*>(cp) = val;
         } else {
+#pragma unroll
             for (int i = 0; i < EPC; ++i) {
                 if (n + i < N) {
                     if constexpr (OUT == DT_F32) reinterpret_cast<uint32_t*>(cp)[i] = val[i];
@@ -71,43 +75,67 @@ __device__ __forceinline__ void quantize_group(const GemmArgs& g, float (&v)[32]
     g.qscales[m * (g.N / 32) + n / 32] = (uint8_t)s;
 }
 
-// Epilogue of big_tile<.., GATED>: acc[0] and acc[1] are g and u of TS rows x TS / 2 columns. Each of what
-// is written is staged through LDS in fp32, so that stores are whole pieces of rows and a lane finds the 32
-// columns of a group.
+// Epilogue of big_tile<.., GATED>: acc[0] and acc[1] are g and u of TS rows x TS / 2 columns. What is written is
+// staged through LDS first, so that stores are whole pieces of rows and a lane finds the 32 columns of a group:
+// g and u side by side in bf16, everything else a tile at a time, h in fp32 where it is quantized.
 template <bool FP8, int OUT, int FQ, int TS>
 __device__ __forceinline__ void gated_epilogue(const GemmArgs& g, v16f (&acc)[Big<FP8, TS>::WTN][Big<FP8, TS>::WTM],
                                                int64_t m0, int64_t n0, uint8_t* smem) {
     using C = Big<FP8, TS>;
-    constexpr int COLS = TS / 2, EP = 4 * COLS + 16;  // staged row pitch
+    constexpr int COLS = TS / 2, ESZ = OUT == DT_F32 ? 4 : 2;
+    constexpr int EP = 4 * COLS + 16, HP = 2 * COLS + 16;  // row pitches: fp32, or g and u in bf16; h in bf16
     static_assert(C::TM * EP <= C::NST * C::STAGE, "staging buffer exceeds the stage buffers");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
     const int fr = lane & 31, fg = lane >> 5;
-    auto stage = [&](auto value) {
+    // four consecutive columns of a row at a time: put(row, column, the four values of acc's index)
+    auto each = [&](auto put) {
         barrier_only();  // every wave is done with the stage buffers / the last pass
 #pragma unroll
         for (int im = 0; im < C::WTM; ++im)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int row = wm * 32 * C::WTM + 32 * im + fr;
-                f32x4 v;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = value(im, 4 * q + i);
-                *reinterpret_cast<f32x4*>(smem + row * EP + 4 * (32 * wn + 8 * q + 4 * fg)) = v;
-            }
+            for (int q = 0; q < 4; ++q) put(wm * 32 * C::WTM + 32 * im + fr, 32 * wn + 8 * q + 4 * fg, im, 4 * q);
         wait_lgkm0();
         barrier_only();
     };
+    auto put_f32 = [&](int row, int col, f32x4 v) { *reinterpret_cast<f32x4*>(smem + row * EP + 4 * col) = v; };
+    auto put_bf16 = [&](int pitch, int row, int col, f32x4 v) {
+        *reinterpret_cast<u32x2*>(smem + row * pitch + 2 * col) = (u32x2){pack_bf16x2_rne(v[0], v[1]), pack_bf16x2_rne(v[2], v[3])};
+    };
+    auto four = [&](int p, int im, int i) { return (f32x4){acc[p][im][i], acc[p][im][i + 1], acc[p][im][i + 2], acc[p][im][i + 3]}; };
+    auto h_of = [&](int im, int i) {
+        f32x4 v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = act_value(acc[0][im][i + k], g.act) * acc[1][im][i + k];
+        return v;
+    };
     if (g.gu) {
         char* const gu = reinterpret_cast<char*>(g.gu);
-        constexpr int ESZ = OUT == DT_F32 ? 4 : 2;
-        stage([&](int im, int i) { return acc[0][im][i]; });
-        store_staged<OUT, C::TM, COLS, C::NTH>(smem, EP, gu, g.ldgu, m0, n0, g.M, g.N);
-        stage([&](int im, int i) { return acc[1][im][i]; });
-        store_staged<OUT, C::TM, COLS, C::NTH>(smem, EP, gu + g.N * ESZ, g.ldgu, m0, n0, g.M, g.N);
+        if constexpr (OUT == DT_BF16) {
+            each([&](int row, int col, int im, int i) {
+                put_bf16(EP, row, col, four(0, im, i));
+                put_bf16(EP, row, COLS + col, four(1, im, i));
+            });
+            store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem, EP, gu, g.ldgu, m0, n0, g.M, g.N);
+            store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem + 2 * COLS, EP, gu + g.N * ESZ, g.ldgu, m0, n0, g.M, g.N);
+        } else {
+            each([&](int row, int col, int im, int i) { put_f32(row, col, four(0, im, i)); });
+            store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem, EP, gu, g.ldgu, m0, n0, g.M, g.N);
+            each([&](int row, int col, int im, int i) { put_f32(row, col, four(1, im, i)); });
+            store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem, EP, gu + g.N * ESZ, g.ldgu, m0, n0, g.M, g.N);
+        }
     }
-    stage([&](int im, int i) { return act_value(acc[0][im][i], g.act) * acc[1][im][i]; });
+    char* const h = reinterpret_cast<char*>(g.c);
+    if constexpr (FQ == FQ_NONE) {
+        if (!h && !g.h32) return;
+        if (OUT == DT_BF16 && !g.h32) {
+            each([&](int row, int col, int im, int i) { put_bf16(HP, row, col, h_of(im, i)); });
+            store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem, HP, h, g.ldc, m0, n0, g.M, g.N);
+            return;
+        }
+    }
+    each([&](int row, int col, int im, int i) { put_f32(row, col, h_of(im, i)); });
     if constexpr (FQ != FQ_NONE) {
         constexpr int GPR = COLS / 32;  // groups of a row, in consecutive lanes
 #pragma unroll 1
@@ -123,8 +151,8 @@ __device__ __forceinline__ void gated_epilogue(const GemmArgs& g, v16f (&acc)[Bi
             quantize_group(g, v, m0 + r, n0 + 32 * j);
         }
     }
-    if (g.c) store_staged<OUT, C::TM, COLS, C::NTH>(smem, EP, reinterpret_cast<char*>(g.c), g.ldc, m0, n0, g.M, g.N);
-    if (g.h32) store_staged<DT_F32, C::TM, COLS, C::NTH>(smem, EP, reinterpret_cast<char*>(g.h32), g.N, m0, n0, g.M, g.N);
+    if (h) store_staged<OUT, DT_F32, C::TM, COLS, C::NTH>(smem, EP, h, g.ldc, m0, n0, g.M, g.N);
+    if (g.h32) store_staged<DT_F32, DT_F32, C::TM, COLS, C::NTH>(smem, EP, reinterpret_cast<char*>(g.h32), g.N, m0, n0, g.M, g.N);
 }
 
 template <bool FP8, bool B2D, int OUT, int FQ, int TS>

@@ -156,10 +156,13 @@ __device__ __forceinline__ void piece_quantize(const QuantOut& q, float (&v)[8],
     if (valid && !(__lane_id() & 3)) q.scales[idx >> 5] = (uint8_t)(k + 127);
 }
 
-// The activation of a gated feed-forward and its derivative.
+// The activation of a gated feed-forward and its derivative. 1 / (1 + e^-x) by the hardware's exponential and
+// reciprocal, an ulp each (2^-22 of the result with the argument's rounding, growing with |x| as e^-x does): the exact
+// quotient takes three times the instructions, which is what bounds the tiles' epilogue (4096 rows, K 4096, F 11008:
+// see gated.hip).
 constexpr float kSqrt2OverPi = 0.79788456080286536f, kGeluCubic = 0.044715f;
 
-__device__ __forceinline__ float sigmoidf(float x) { return 1.0f / (1.0f + __expf(-x)); }
+__device__ __forceinline__ float sigmoidf(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
 __device__ __forceinline__ float act_value(float g, int act) {
     if (act == ACT_SILU) return g * sigmoidf(g);
