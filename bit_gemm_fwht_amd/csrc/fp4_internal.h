@@ -111,6 +111,7 @@ struct GemmArgs {
     int64_t ldgu;
     float* h32;              // [M, N] fp32 for a quantize pass of its own, or NULL
     int act;
+    int c_nt;                // c goes past the caches
 };
 
 // NVFP4 [rows, cols] -> E4M3 [rows, cols] + E8M0 [rows, cols / 32] (the GEMM's FP8 re-expression)

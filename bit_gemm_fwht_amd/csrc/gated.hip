@@ -18,8 +18,11 @@ namespace bgf {
 
 // Store a staged tile [ROWS][COLS] of dtype OUT (SRC: as it is staged, OUT or fp32; row pitch `pitch` bytes in LDS)
 // at c[m0 ..][n0 ..], 16-byte pieces where the place allows; rows from M and columns from N on are not there. A
-// thread keeps its piece of the columns and walks down the rows.
-template <int OUT, int SRC, int ROWS, int COLS, int NTH>
+// thread keeps its piece of the columns and walks down the rows. NT: past the caches, which then keep the operands
+// that other tiles read again: g and u always (they wait for the backward pass), h where it would not stay in them
+// until it is read either. 4096 rows, K 4096, F 11008 in 4 bits with the next quantize of h: 320 us with nothing past
+// the caches, 320 with g and u, 278 with all three; 2048 rows: 170, 138, 143.
+template <int OUT, int SRC, int ROWS, int COLS, int NTH, bool NT = false>
 __device__ __forceinline__ void store_staged(const uint8_t* lds, int pitch, char* c, int64_t ldc, int64_t m0, int64_t n0,
                                              int64_t M, int64_t N) {
     constexpr int ESZ = OUT == DT_F32 ? 4 : 2, EPC = 16 / ESZ, PPR = COLS / EPC;
@@ -42,7 +45,8 @@ __device__ __forceinline__ void store_staged(const uint8_t* lds, int pitch, char
         }
         char* cp = c + (m * ldc + n) * ESZ;
         if (vec_ok && n + EPC <= N) {
-            *reinterpret_cast<u32x4*>(cp) = val;
+            if constexpr (NT) __builtin_nontemporal_store(val, reinterpret_cast<u32x4*>(cp));
+            else *reinterpret_cast<u32x4*>(cp) = val;
         } else {
 #pragma unroll
             for (int i = 0; i < EPC; ++i) {
@@ -117,13 +121,13 @@ __device__ __forceinline__ void gated_epilogue(const GemmArgs& g, v16f (&acc)[Bi
                 put_bf16(EP, row, col, four(0, im, i));
                 put_bf16(EP, row, COLS + col, four(1, im, i));
             });
-            store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem, EP, gu, g.ldgu, m0, n0, g.M, g.N);
-            store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem + 2 * COLS, EP, gu + g.N * ESZ, g.ldgu, m0, n0, g.M, g.N);
+            store_staged<OUT, OUT, C::TM, COLS, C::NTH, true>(smem, EP, gu, g.ldgu, m0, n0, g.M, g.N);
+            store_staged<OUT, OUT, C::TM, COLS, C::NTH, true>(smem + 2 * COLS, EP, gu + g.N * ESZ, g.ldgu, m0, n0, g.M, g.N);
         } else {
             each([&](int row, int col, int im, int i) { put_f32(row, col, four(0, im, i)); });
-            store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem, EP, gu, g.ldgu, m0, n0, g.M, g.N);
+            store_staged<OUT, OUT, C::TM, COLS, C::NTH, true>(smem, EP, gu, g.ldgu, m0, n0, g.M, g.N);
             each([&](int row, int col, int im, int i) { put_f32(row, col, four(1, im, i)); });
-            store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem, EP, gu + g.N * ESZ, g.ldgu, m0, n0, g.M, g.N);
+            store_staged<OUT, OUT, C::TM, COLS, C::NTH, true>(smem, EP, gu + g.N * ESZ, g.ldgu, m0, n0, g.M, g.N);
         }
     }
     char* const h = reinterpret_cast<char*>(g.c);
@@ -131,7 +135,8 @@ __device__ __forceinline__ void gated_epilogue(const GemmArgs& g, v16f (&acc)[Bi
         if (!h && !g.h32) return;
         if (OUT == DT_BF16 && !g.h32) {
             each([&](int row, int col, int im, int i) { put_bf16(HP, row, col, h_of(im, i)); });
-            store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem, HP, h, g.ldc, m0, n0, g.M, g.N);
+            if (g.c_nt) store_staged<OUT, OUT, C::TM, COLS, C::NTH, true>(smem, HP, h, g.ldc, m0, n0, g.M, g.N);
+            else store_staged<OUT, OUT, C::TM, COLS, C::NTH>(smem, HP, h, g.ldc, m0, n0, g.M, g.N);
             return;
         }
     }
@@ -151,7 +156,10 @@ __device__ __forceinline__ void gated_epilogue(const GemmArgs& g, v16f (&acc)[Bi
             quantize_group(g, v, m0 + r, n0 + 32 * j);
         }
     }
-    if (h) store_staged<OUT, DT_F32, C::TM, COLS, C::NTH>(smem, EP, h, g.ldc, m0, n0, g.M, g.N);
+    if (h) {
+        if (g.c_nt) store_staged<OUT, DT_F32, C::TM, COLS, C::NTH, true>(smem, EP, h, g.ldc, m0, n0, g.M, g.N);
+        else store_staged<OUT, DT_F32, C::TM, COLS, C::NTH>(smem, EP, h, g.ldc, m0, n0, g.M, g.N);
+    }
     if (g.h32) store_staged<DT_F32, DT_F32, C::TM, COLS, C::NTH>(smem, EP, reinterpret_cast<char*>(g.h32), g.N, m0, n0, g.M, g.N);
 }
 
@@ -592,6 +600,7 @@ static hipError_t launch_gated_o(const GemmArgs& g, int kind, int kernel, int fu
 
 hipError_t launch_gated(GemmArgs g, const GatedPlan& p, int kind, int dtype, int fused_q, void* ws, hipStream_t s) {
     g.h32 = p.quant_pass ? reinterpret_cast<float*>(ws) : nullptr;
+    g.c_nt = g.M * g.N * (dtype == DT_BF16 ? 2 : 4) >= (int64_t(64) << 20);
     const int fused = fused_q && !p.quant_pass;
     const hipError_t e = dtype == DT_BF16 ? launch_gated_o<DT_BF16>(g, kind, p.kernel, fused, s) : launch_gated_o<DT_F32>(g, kind, p.kernel, fused, s);
     if (e != hipSuccess || !p.quant_pass) return e;
@@ -608,26 +617,30 @@ hipError_t launch_gated(GemmArgs g, const GatedPlan& p, int kind, int dtype, int
 }
 
 // ---------------------------------------------------------------------------------------------
-// Backward: dgu = (dh u act'(g), dh act(g)), a piece of 8 columns of both a lane.
+// Backward: dgu = (dh u act'(g), dh act(g)), a piece of 8 columns of both a lane; bound by memory. NT (bf16): what
+// is read and dgu go past the caches, where the call is larger than what they keep (4096 rows, F 11008: 93.5 us
+// against 99.4; 1024 rows 27.1 against 27.7, but then dgu is still there for the calls that read it next).
 // ---------------------------------------------------------------------------------------------
-template <int DT, int FQ>
+template <int DT, int FQ, bool NT>
 __global__ __launch_bounds__(256) void k_gated_grad(GatedGradArgs a) {
     const int pieces = a.F >> 3;
     const int64_t total = a.rows * pieces;
     for (int64_t b0 = (int64_t)blockIdx.x * 256; b0 < total; b0 += (int64_t)gridDim.x * 256) {
-        const int64_t i = b0 + threadIdx.x;
-        const bool in = i < total;
-        const int64_t row = i / pieces;
-        const int col = 8 * (int)(i - row * pieces);
+        const bool in = b0 + threadIdx.x < total;
+        // one 64-bit division a wave, a 32-bit one a lane
+        const int64_t row0 = b0 / pieces;
+        const uint32_t i = (uint32_t)(b0 - row0 * pieces) + threadIdx.x, down = i / (uint32_t)pieces;
+        const int64_t row = row0 + down;
+        const int col = 8 * (int)(i - down * (uint32_t)pieces);
         float dh[8], g[8], u[8];
         if (in) {
-            Piece<DT> p;
-            piece_load<DT>(p, a.dh, row * a.lddh + col);
+            Piece<DT> p, q, r;
+            piece_load<DT, NT>(p, a.dh, row * a.lddh + col);
+            piece_load<DT, NT>(q, a.gu, row * a.ldgu + col);
+            piece_load<DT, NT>(r, a.gu, row * a.ldgu + a.F + col);
             piece_values<DT>(p, dh);
-            piece_load<DT>(p, a.gu, row * a.ldgu + col);
-            piece_values<DT>(p, g);
-            piece_load<DT>(p, a.gu, row * a.ldgu + a.F + col);
-            piece_values<DT>(p, u);
+            piece_values<DT>(q, g);
+            piece_values<DT>(r, u);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) dh[j] = g[j] = u[j] = 0.0f;
@@ -640,8 +653,8 @@ __global__ __launch_bounds__(256) void k_gated_grad(GatedGradArgs a) {
             u[j] = dh[j] * v;
         }
         if (a.dgu && in) {
-            piece_store<DT>(a.dgu, row * a.lddgu + col, piece_pack<DT>(g));
-            piece_store<DT>(a.dgu, row * a.lddgu + a.F + col, piece_pack<DT>(u));
+            piece_store<DT, NT>(a.dgu, row * a.lddgu + col, piece_pack<DT>(g));
+            piece_store<DT, NT>(a.dgu, row * a.lddgu + a.F + col, piece_pack<DT>(u));
         }
         if constexpr (FQ != FQ_NONE) {
             constexpr int RND = FQ == FQ_SR ? RND_SR : RND_RNE;
@@ -651,18 +664,19 @@ __global__ __launch_bounds__(256) void k_gated_grad(GatedGradArgs a) {
     }
 }
 
-template <int DT>
+template <int DT, bool NT>
 static hipError_t launch_gated_grad_k(const GatedGradArgs& a, int rnd, hipStream_t s) {
     const int64_t need = (a.rows * (a.F / 8) + 255) / 256;
     const unsigned grid = (unsigned)(need < kMaxGrid ? need : kMaxGrid);
-    if (!a.q.codes) hipLaunchKernelGGL((k_gated_grad<DT, FQ_NONE>), dim3(grid), dim3(256), 0, s, a);
-    else if (rnd == RND_SR) hipLaunchKernelGGL((k_gated_grad<DT, FQ_SR>), dim3(grid), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_gated_grad<DT, FQ_RNE>), dim3(grid), dim3(256), 0, s, a);
+    if (!a.q.codes) hipLaunchKernelGGL((k_gated_grad<DT, FQ_NONE, NT>), dim3(grid), dim3(256), 0, s, a);
+    else if (rnd == RND_SR) hipLaunchKernelGGL((k_gated_grad<DT, FQ_SR, NT>), dim3(grid), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_gated_grad<DT, FQ_RNE, NT>), dim3(grid), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_gated_grad(const GatedGradArgs& a, int dtype, int rnd, hipStream_t s) {
-    return dtype == DT_BF16 ? launch_gated_grad_k<DT_BF16>(a, rnd, s) : launch_gated_grad_k<DT_F32>(a, rnd, s);
+    if (dtype == DT_F32) return launch_gated_grad_k<DT_F32, false>(a, rnd, s);
+    return a.rows * a.F * 6 >= (int64_t(96) << 20) ? launch_gated_grad_k<DT_BF16, true>(a, rnd, s) : launch_gated_grad_k<DT_BF16, false>(a, rnd, s);
 }
 
 }  // namespace bgf

@@ -245,7 +245,7 @@ int fp4_rope(const fp4_rope_args* r, void* stream) {
         if (!std::isfinite(r->scale) || !r->inv_freq || (r->positions && r->batch)) return FP4_ERR_INVALID_ARG;
         if (!r->positions && !r->batch && r->tokens > 0) return FP4_ERR_INVALID_ARG;
         const int64_t heads = (int64_t)r->heads[0] + r->heads[1];
-        if (r->head_dim > 1024 || heads > 65536 || r->tokens > kMaxRows || r->tokens * heads > kMaxRows) return FP4_ERR_UNSUPPORTED;
+        if (r->head_dim > 1024 || r->head_dim % 2 || heads > 65536 || r->tokens > kMaxRows || r->tokens * heads > kMaxRows) return FP4_ERR_UNSUPPORTED;
         if (!aligned(r->inv_freq, 8) || !aligned(r->positions, 4)) return FP4_ERR_ALIGNMENT;
         RopeArgs a{};
         if (r->batch) {

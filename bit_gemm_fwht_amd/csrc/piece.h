@@ -56,11 +56,14 @@ __device__ __forceinline__ Piece<DT> piece_pack(const float (&v)[8]) {
     return p;
 }
 
-template <int DT>
+template <int DT, bool NT = false>
 __device__ __forceinline__ void piece_store(void* base, int64_t elem, const Piece<DT>& p) {
     u32x4* d = reinterpret_cast<u32x4*>(reinterpret_cast<char*>(base) + elem * (DT == DT_BF16 ? 2 : 4));
 #pragma unroll
-    for (int i = 0; i < Piece<DT>::N; ++i) d[i] = p.w[i];
+    for (int i = 0; i < Piece<DT>::N; ++i) {
+        if constexpr (NT) __builtin_nontemporal_store(p.w[i], d + i);
+        else d[i] = p.w[i];
+    }
 }
 
 // One stage of the rotation between lanes l and l ^ M: a + b in the lower lane, a - b in the upper.

@@ -1,8 +1,8 @@
 // Rotary positions: the channels of a head turned in pairs by position * inv_freq[i].
 //
 // A workgroup takes a few tokens. First it computes their angles' sines and cosines, one (token, pair) a
-// thread and for all heads at once, into LDS; then its threads walk over the tokens' heads, a unit of V pairs
-// at a time. The angle is fp64 and so is its reduction to a quarter turn (an fp32 product of a position past
+// thread and for all heads at once, into LDS; then its threads walk over the tokens' heads in units of 16 bytes
+// (half layout: 16 and their partners). The angle is fp64 and so is its reduction to a quarter turn (an fp32 product of a position past
 // 2^17 is off by 2^-7 radians); sine and cosine of what is left, |r| <= pi / 4, are fp32 Taylor sums.
 #include "device.h"
 #include "kv_device.h"
@@ -32,84 +32,65 @@ __device__ __forceinline__ float2 cos_sin(double t) {
     return make_float2(q == 1 || q == 2 ? -cs : cs, q >= 2 ? -sn : sn);
 }
 
-// V consecutive values, in accesses of 16 bytes or V * size where that is less
+// V consecutive values in one access of V * size bytes
 template <int DT, int V>
+struct Words {
+    typedef uint32_t type __attribute__((ext_vector_type(DT == DT_BF16 ? V / 2 : V)));
+};
+template <int DT, int V, bool NT>
 __device__ __forceinline__ void load_values(const void* base, int64_t at, float (&v)[V]) {
-    if constexpr (DT == DT_BF16) {
-        constexpr int S = V > 8 ? 8 : V;
-        typedef uint16_t words __attribute__((ext_vector_type(S)));
-        const uint16_t* s = reinterpret_cast<const uint16_t*>(base) + at;
-        if constexpr (V == 1) {
-            v[0] = __uint_as_float((uint32_t)s[0] << 16);
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; k += S) {
-                const words w = *reinterpret_cast<const words*>(s + k);
-#pragma unroll
-                for (int i = 0; i < S; ++i) v[k + i] = __uint_as_float((uint32_t)w[i] << 16);
-            }
-        }
+    if constexpr (DT == DT_BF16 && V == 1) {
+        v[0] = __uint_as_float((uint32_t)(reinterpret_cast<const uint16_t*>(base)[at]) << 16);
+    } else if constexpr (V == (DT == DT_BF16 ? 2 : 1)) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(base) + at * (DT == DT_BF16 ? 2 : 4));
+        if constexpr (DT == DT_BF16) v[0] = bf16_lo(w), v[1] = bf16_hi(w);
+        else v[0] = __uint_as_float(w);
     } else {
-        constexpr int S = V > 4 ? 4 : V;
-        typedef float words __attribute__((ext_vector_type(S)));
-        const float* s = reinterpret_cast<const float*>(base) + at;
-        if constexpr (V == 1) {
-            v[0] = s[0];
-        } else {
+        typedef typename Words<DT, V>::type words;
+        const words* s = reinterpret_cast<const words*>(reinterpret_cast<const char*>(base) + at * (DT == DT_BF16 ? 2 : 4));
+        const words w = NT ? __builtin_nontemporal_load(s) : *s;
 #pragma unroll
-            for (int k = 0; k < V; k += S) {
-                const words w = *reinterpret_cast<const words*>(s + k);
-#pragma unroll
-                for (int i = 0; i < S; ++i) v[k + i] = w[i];
-            }
+        for (int i = 0; i < V; ++i) {
+            if constexpr (DT == DT_BF16) v[i] = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+            else v[i] = __uint_as_float(w[i]);
         }
     }
 }
 
-template <int DT, int V>
+template <int DT, int V, bool NT>
 __device__ __forceinline__ void store_values(void* base, int64_t at, const float (&v)[V]) {
-    if constexpr (DT == DT_BF16) {
-        uint16_t* d = reinterpret_cast<uint16_t*>(base) + at;
-        if constexpr (V == 1) {
-            d[0] = (uint16_t)pack_bf16x2_rne(v[0], 0.0f);
-        } else {
-            constexpr int S = V > 8 ? 8 : V;
-            typedef uint32_t words __attribute__((ext_vector_type(S / 2)));
-#pragma unroll
-            for (int k = 0; k < V; k += S) {
-                words w;
-#pragma unroll
-                for (int i = 0; i < S / 2; ++i) w[i] = pack_bf16x2_rne(v[k + 2 * i], v[k + 2 * i + 1]);
-                *reinterpret_cast<words*>(d + k) = w;
-            }
-        }
+    if constexpr (DT == DT_BF16 && V == 1) {
+        reinterpret_cast<uint16_t*>(base)[at] = (uint16_t)pack_bf16x2_rne(v[0], 0.0f);
+    } else if constexpr (V == (DT == DT_BF16 ? 2 : 1)) {
+        uint32_t* d = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(base) + at * (DT == DT_BF16 ? 2 : 4));
+        if constexpr (DT == DT_BF16) *d = pack_bf16x2_rne(v[0], v[1]);
+        else *d = __float_as_uint(v[0]);
     } else {
-        constexpr int S = V > 4 ? 4 : V;
-        typedef float words __attribute__((ext_vector_type(S)));
-        float* d = reinterpret_cast<float*>(base) + at;
-        if constexpr (V == 1) {
-            d[0] = v[0];
-        } else {
+        typedef typename Words<DT, V>::type words;
+        words* d = reinterpret_cast<words*>(reinterpret_cast<char*>(base) + at * (DT == DT_BF16 ? 2 : 4));
+        words w;
 #pragma unroll
-            for (int k = 0; k < V; k += S) {
-                words w;
-#pragma unroll
-                for (int i = 0; i < S; ++i) w[i] = v[k + i];
-                *reinterpret_cast<words*>(d + k) = w;
-            }
+        for (int i = 0; i < V; i += 2) {
+            if constexpr (DT == DT_BF16) w[i >> 1] = pack_bf16x2_rne(v[i], v[i + 1]);
+            else w[i] = __float_as_uint(v[i]), w[i + 1] = __float_as_uint(v[i + 1]);
         }
+        if constexpr (NT) __builtin_nontemporal_store(w, d);
+        else *d = w;
     }
 }
 
-// HALF: pairs (i, i + rot / 2), else (2 i, 2 i + 1). A unit is V pairs of one head of one token. Channels
-// past rot are copied V at a time (where they are not in place already).
-template <int DT, bool HALF, int V>
+// HALF: pairs (i, i + rot / 2), a unit is V channels and their V partners; else (2 i, 2 i + 1), a unit is V channels
+// (V even). Units past the turned ones copy V channels (where they are not in place already).
+template <int DT, bool HALF, int V, bool NT>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a, int per) {
     __shared__ float2 turn[kRopePairs];
     __shared__ int pos[kRopeTokens];
     __shared__ int there[kRopeTokens];
     const int half = a.rot >> 1, heads = a.heads[0] + a.heads[1];
-    const int units = half / V, rest = (a.dim - a.rot) / V;
+    const int turned = (HALF ? half : a.rot) / V, units = turned + (a.dim - a.rot) / V;
+    // a thread's unit, head and token; kRopeThreads units further on it is (step_u, step_h, step_t) more
+    const int u0 = threadIdx.x % units, r0 = threadIdx.x / units;
+    const int step_u = kRopeThreads % units, step_r = kRopeThreads / units, step_h = step_r % heads, step_t = step_r / heads;
     for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < a.tokens; t0 += (int64_t)gridDim.x * per) {
         const int n = (int)min((int64_t)per, a.tokens - t0);
         __syncthreads();  // the last tokens' values have been read
@@ -142,66 +123,90 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a, int per) {
             turn[i] = cs;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < n * heads * units; i += kRopeThreads) {
-            const int u = i % units, h = (i / units) % heads, tok = i / units / heads;
-            if (!there[tok]) continue;
+        int u = u0, h = r0 % heads, tok = r0 / heads;
+        while (tok < n) {
             const int k = h >= a.heads[0], hk = h - (k ? a.heads[0] : 0);
             const int64_t t = t0 + tok;
             const int64_t xi = t * a.ldx[k] + hk * a.ldx_head[k], oi = t * a.ldo[k] + hk * a.ldo_head[k];
-            const float2* cs = turn + tok * half + u * V;
-            if constexpr (HALF) {
-                float x1[V], x2[V], y1[V], y2[V];
-                load_values<DT, V>(a.x[k], xi + u * V, x1);
-                load_values<DT, V>(a.x[k], xi + half + u * V, x2);
+            // lanes that turn and lanes that copy load and store together
+            const bool turns = u < turned, same = a.out[k] == a.x[k];
+            if (there[tok] && (turns || !same)) {
+                const int c = HALF && !turns ? a.rot + (u - turned) * V : u * V;
+                float x[V], y[V];
+                load_values<DT, V, NT>(a.x[k], xi + c, x);
+                if constexpr (HALF) {
+                    float z[V] = {};
+                    if (turns) load_values<DT, V, NT>(a.x[k], xi + half + c, z);
+                    const float2* cs = turn + (turns ? tok * half + c : 0);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float2 c = cs[j];
-                    y1[j] = __builtin_fmaf(x1[j], c.x, -(x2[j] * c.y));
-                    y2[j] = __builtin_fmaf(x2[j], c.x, x1[j] * c.y);
-                }
-                store_values<DT, V>(a.out[k], oi + u * V, y1);
-                store_values<DT, V>(a.out[k], oi + half + u * V, y2);
-            } else {
-                float x[2 * V], y[2 * V];
-                load_values<DT, 2 * V>(a.x[k], xi + 2 * u * V, x);
+                    for (int j = 0; j < V; ++j) {
+                        const float2 s = cs[turns ? j : 0];
+                        y[j] = turns ? __builtin_fmaf(x[j], s.x, -(z[j] * s.y)) : x[j];
+                        z[j] = __builtin_fmaf(z[j], s.x, x[j] * s.y);
+                    }
+                    store_values<DT, V, NT>(a.out[k], oi + c, y);
+                    if (turns) store_values<DT, V, NT>(a.out[k], oi + half + c, z);
+                } else {
+                    const float2* cs = turn + (turns ? tok * half + c / 2 : 0);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float2 c = cs[j];
-                    y[2 * j] = __builtin_fmaf(x[2 * j], c.x, -(x[2 * j + 1] * c.y));
-                    y[2 * j + 1] = __builtin_fmaf(x[2 * j + 1], c.x, x[2 * j] * c.y);
+                    for (int j = 0; j < V; j += 2) {
+                        const float2 s = cs[turns ? j / 2 : 0];
+                        y[j] = turns ? __builtin_fmaf(x[j], s.x, -(x[j + 1] * s.y)) : x[j];
+                        y[j + 1] = turns ? __builtin_fmaf(x[j + 1], s.x, x[j] * s.y) : x[j + 1];
+                    }
+                    store_values<DT, V, NT>(a.out[k], oi + c, y);
                 }
-                store_values<DT, 2 * V>(a.out[k], oi + 2 * u * V, y);
             }
-        }
-        for (int i = threadIdx.x; i < n * heads * rest; i += kRopeThreads) {
-            const int u = i % rest, h = (i / rest) % heads, tok = i / rest / heads;
-            const int k = h >= a.heads[0], hk = h - (k ? a.heads[0] : 0);
-            if (!there[tok] || a.out[k] == a.x[k]) continue;
-            const int64_t t = t0 + tok;
-            float x[V];
-            load_values<DT, V>(a.x[k], t * a.ldx[k] + hk * a.ldx_head[k] + a.rot + u * V, x);
-            store_values<DT, V>(a.out[k], t * a.ldo[k] + hk * a.ldo_head[k] + a.rot + u * V, x);
+            u += step_u;
+            h += step_h;
+            tok += step_t;
+            if (u >= units) {
+                u -= units;
+                ++h;
+            }
+            if (h >= heads) {  // h < 2 heads: one step is enough
+                h -= heads;
+                ++tok;
+            }
         }
     }
 }
 
-template <int DT, bool HALF>
+template <int DT, bool HALF, bool NT>
 static hipError_t launch_rope_k(const RopeArgs& a, hipStream_t s) {
     const int half = a.rot / 2;
     int per = kRopePairs / half;
     if (per > 4) per = 4;
     const int64_t need = (a.tokens + per - 1) / per;
-    const unsigned grid = (unsigned)(need < kMaxGrid ? need : kMaxGrid);
-    // pairs of a unit: as many as fill 16-byte accesses and divide both parts of a head (their places then are
-    // multiples of the access too)
-    if (half % 8 == 0 && (a.dim - a.rot) % 8 == 0) hipLaunchKernelGGL((k_rope<DT, HALF, 8>), dim3(grid), dim3(kRopeThreads), 0, s, a, per);
-    else hipLaunchKernelGGL((k_rope<DT, HALF, 1>), dim3(grid), dim3(kRopeThreads), 0, s, a, per);
+    const dim3 grid((unsigned)(need < kMaxGrid ? need : kMaxGrid)), block(kRopeThreads);
+    // a unit: 16 bytes, or as many as divide both parts of a head (whose places are then multiples of it too)
+    constexpr int most = DT == DT_BF16 ? 8 : 4;
+    int v = most;
+    while ((HALF ? half : a.rot) % v || (a.dim - a.rot) % v) v /= 2;
+    if (v == most) hipLaunchKernelGGL((k_rope<DT, HALF, most, NT>), grid, block, 0, s, a, per);
+    else if (v == most / 2) hipLaunchKernelGGL((k_rope<DT, HALF, most / 2, NT>), grid, block, 0, s, a, per);
+    else if constexpr (DT == DT_BF16) {
+        if (v == 2) hipLaunchKernelGGL((k_rope<DT, HALF, 2, NT>), grid, block, 0, s, a, per);
+        else if constexpr (HALF) hipLaunchKernelGGL((k_rope<DT, HALF, 1, NT>), grid, block, 0, s, a, per);
+    } else if constexpr (HALF) {
+        hipLaunchKernelGGL((k_rope<DT, HALF, 1, NT>), grid, block, 0, s, a, per);
+    }
     return hipGetLastError();
 }
 
+template <int DT, bool HALF>
+static hipError_t launch_rope_h(const RopeArgs& a, hipStream_t s) {
+    // past the caches where the call is larger than what they keep and a unit's runs are whole cache lines, which
+    // partly written ones would not be twice (16384 tokens of 40 heads of 128: half layout 61.2 us against 67.3,
+    // interleaved 62.8 against 69.7; heads of 80, half layout: 61.3 against 48.7, interleaved 42.1 against 47.8)
+    const int64_t bytes = a.tokens * (a.heads[0] + a.heads[1]) * a.dim * (DT == DT_BF16 ? 2 : 4);
+    const bool lines = !HALF || (a.rot / 2) * (DT == DT_BF16 ? 2 : 4) % 128 == 0;
+    return bytes >= (int64_t(64) << 20) && lines ? launch_rope_k<DT, HALF, true>(a, s) : launch_rope_k<DT, HALF, false>(a, s);
+}
+
 hipError_t launch_rope(const RopeArgs& a, int dtype, int layout, hipStream_t s) {
-    if (dtype == DT_BF16) return layout ? launch_rope_k<DT_BF16, false>(a, s) : launch_rope_k<DT_BF16, true>(a, s);
-    return layout ? launch_rope_k<DT_F32, false>(a, s) : launch_rope_k<DT_F32, true>(a, s);
+    if (dtype == DT_BF16) return layout ? launch_rope_h<DT_BF16, false>(a, s) : launch_rope_h<DT_BF16, true>(a, s);
+    return layout ? launch_rope_h<DT_F32, false>(a, s) : launch_rope_h<DT_F32, true>(a, s);
 }
 
 }  // namespace bgf

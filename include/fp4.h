@@ -472,8 +472,8 @@ int fp4_rmsnorm_backward(const fp4_norm_grad* n, void* workspace, int64_t ws_byt
  * Positions: int32 [tokens] (positions), or those of a cache's batch (batch: of the batch's fields cu_tokens,
  * context, seqs and tokens are used): row i of a sequence with n rows sits at context - n + i. Rows with no
  * token (before a sequence's first, behind the last sequence) are left as they are. Exactly one of the two
- * is given. out[i] may be x[i] itself (then of the same strides). Strides as for fp4_kv_append. head_dim up
- * to 1024, rotary_dim even, at most head_dim; tokens * heads below 2^31. */
+ * is given. out[i] may be x[i] itself (then of the same strides). Strides as for fp4_kv_append. head_dim
+ * even, up to 1024, rotary_dim even, at most head_dim; tokens * heads below 2^31. */
 enum { FP4_ROPE_HALF = 0, FP4_ROPE_INTERLEAVED = 1 };
 typedef struct fp4_rope_args {
     const void* x[2];

@@ -263,6 +263,27 @@ def test_rope(layer, dim, rot, interleaved):
             assert torch.equal(a, got[0])
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_copies_the_other_channels_bit_for_bit(layer, interleaved):
+    """Channels past the turned ones, whatever they hold; large enough for every variant of the accesses."""
+    for dtype, dim, rot, tokens in ((torch.bfloat16, 80, 20, 30), (torch.float32, 96, 24, 30), (torch.bfloat16, 128, 64, 20000)):
+        x = rand(gen(2), tokens, 20, dim, dtype=dtype)
+        x[..., rot] = -0.0
+        x[..., rot + 1] = -math.inf
+        x[..., rot + 2] = math.nan
+        f, _ = layer.rotary_frequencies(rot, device="cuda")
+        rotary = layer.Rotary(f, layout=layer.INTERLEAVED if interleaved else layer.HALF)
+        pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+        y = layer.rope(x, rotary, pos)
+        bits = torch.int16 if dtype is torch.bfloat16 else torch.int32
+        assert torch.equal(y[..., rot:].contiguous().view(bits), x[..., rot:].contiguous().view(bits))
+        part = layer.rope(x[:29].contiguous(), rotary, pos[:29])
+        assert torch.equal(y[:29, :, :rot], part[..., :rot])
+        a = x.clone()
+        layer.rope(a, rotary, pos, out=a)
+        assert torch.equal(a.view(bits), y.view(bits))
+
+
 def test_rope_batch_positions(layer, kv):
     """Positions of a cache's batch: ragged, empty sequences, rows before a sequence's first token and rows
     behind the last sequence, which keep what was there; slices of one projection, in place and not."""

@@ -146,7 +146,7 @@ def rope(layer, batch=None, **kw):
     (dict(out=(0x30000, None)), "INVALID_ARG"), (dict(ldx=(-512, 256)), "INVALID_ARG"), (dict(out=(0x30000, 0x30000)), "INVALID_ARG"),
     (dict(out=(0x20000, 0x40000)), "INVALID_ARG"), (dict(out=(0x10000, 0x40000), ldo=(1024, 256)), "INVALID_ARG"),
     (dict(ldo=(120, 256)), "INVALID_ARG"), (dict(ldo_head=(64, 128)), "INVALID_ARG"), (dict(ldo=(256, 256)), "INVALID_ARG"),
-    (dict(head_dim=2048), "UNSUPPORTED"), (dict(tokens=1 << 31), "UNSUPPORTED"), (dict(tokens=1 << 62), "UNSUPPORTED"),
+    (dict(head_dim=2048), "UNSUPPORTED"), (dict(head_dim=127), "UNSUPPORTED"), (dict(tokens=1 << 31), "UNSUPPORTED"), (dict(tokens=1 << 62), "UNSUPPORTED"),
     (dict(heads=(70000, 0)), "UNSUPPORTED"), (dict(x=(0x10002, 0x20000)), "ALIGNMENT"), (dict(ldx=(516, 256)), "ALIGNMENT"),
     (dict(inv_freq=0x50004), "ALIGNMENT"), (dict(positions=0x60002), "ALIGNMENT"),
 ])
