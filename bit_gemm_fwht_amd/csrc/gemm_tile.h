@@ -35,8 +35,9 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // TS = 256: 8 waves of 128 x 64 (one workgroup per CU: two 68 KB stages); TS = 128: 4 waves of
 // 64 x 64 (two workgroups per CU: two 34 KB stages each), for grids of 256 x 256 tiles that would
-// leave most CUs idle.
-template <bool FP8, int TS = 256>
+// leave most CUs idle. NS stages: with 4 of them three are on their way while one is multiplied (TS = 128, one
+// workgroup per CU), for grids of so few tiles that each has a CU to itself.
+template <bool FP8, int TS = 256, int NS = 2>
 struct Big {
     static constexpr int TM = TS, TN = TS, NW = TS == 256 ? 8 : 4, NTH = 64 * NW;
     static constexpr int WTM = TS == 256 ? 4 : 2, WTN = 2;  // 32x32 tiles per wave (M x N)
@@ -48,7 +49,7 @@ struct Big {
     static constexpr int CPR = RB / 16;               // 16-byte chunks per row
     static constexpr int NKK = KSTEP / 64;            // 64-deep MFMA steps per stage
     static constexpr int SPR = KSTEP / 32;            // scale bytes per row per stage
-    static constexpr int NST = 2;                     // pipeline stages
+    static constexpr int NST = NS;                    // pipeline stages
     static constexpr int OPB = TM * RB;               // operand bytes per stage
     static constexpr int SB = TM * SPR;               // scale bytes per operand per stage
     // stage layout: A's scales, B's scales, A's codes, B's codes (scales first, so that the
@@ -369,7 +370,7 @@ __device__ __forceinline__ void big_epilogue(const GemmArgs& g, v16f (&acc)[Big<
 }
 
 // Epilogue of the gated feed-forward's tile (gated.hip).
-template <bool FP8, int OUT, int FQ, int TS>
+template <bool FP8, int OUT, int FQ, int TS, int NS>
 __device__ __forceinline__ void gated_epilogue(const GemmArgs& g, v16f (&acc)[Big<FP8, TS>::WTN][Big<FP8, TS>::WTM],
                                                int64_t m0, int64_t n0, uint8_t* smem);
 
@@ -379,9 +380,9 @@ __device__ __forceinline__ void gated_epilogue(const GemmArgs& g, v16f (&acc)[Bi
 // GATED: two products of TS x TS / 2 results with the operands b and b_up, N columns each. The rows of B's
 // slab alternate between the two in groups of 32 (wave column wn: 32 rows of b, then the same 32 of b_up),
 // so that a lane's accumulators of tile 0 and tile 1 are the two products' values of the same place.
-template <bool FP8, bool B2D, int OUT, bool NVG, int FQ, int TS = 256, bool GATED = false>
+template <bool FP8, bool B2D, int OUT, bool NVG, int FQ, int TS = 256, bool GATED = false, int NS = 2>
 __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem) {
-    using C = Big<FP8, TS>;
+    using C = Big<FP8, TS, NS>;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
     const int wm = wave / C::WN, wn = wave % C::WN;
@@ -390,7 +391,9 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint
 
     const int64_t rowbytes = FP8 ? g.K : g.K / 2;
     const int64_t kgroups = g.K / 32;
-    const int KT = (int)(g.K / C::KSTEP);
+    // K is a multiple of a stage's depth; GATED also takes E2M1 rows that end halfway through the last stage
+    const int KT = GATED ? (int)((g.K + C::KSTEP - 1) / C::KSTEP) : (int)(g.K / C::KSTEP);
+    const bool ragged = GATED && g.K % C::KSTEP != 0;
 
     // Direct-to-LDS copies go through buffer resources: base + 32-bit byte offset. The row part of
     // every offset sits in the per-lane (vector) offset, which the range check covers, so rows
@@ -442,34 +445,37 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint
     // stage, so that no wave stalls on a full address FIFO with all its copies at once (part p:
     // A and B copies i in [p IPW / NKK, (p + 1) IPW / NKK); the scales with part 0).
     static_assert(C::IPW % C::NKK == 0, "copies per step");
-    // Stage KT (one past the last) is a dummy: its copies go through the zero-extent resource, so
-    // they read nothing and write zeros into the free stage buffer.
+    // Stages from KT on are dummies: their copies go through the zero-extent resource, so they read
+    // nothing and write zeros into a free stage buffer.
     auto issue_part = [&](int kt, int part) {
         uint8_t* st = smem + (kt % C::NST) * C::STAGE;
         const bool real = kt < KT;
         const int so = real ? kt * C::RB : 0, ss = real ? kt * C::SPR : 0;
         const __amdgpu_buffer_rsrc_t qA = real ? rA : rZ, qB = real ? rB : rZ;
         const __amdgpu_buffer_rsrc_t qSA = real ? rSA : rZ;
+        const bool cut = ragged && kt == KT - 1;  // its upper half is not there: offsets past the extent
         constexpr int IPP = C::IPW / C::NKK;
 #pragma unroll
         for (int ii = 0; ii < IPP; ++ii) {
             const int i = part * IPP + ii;
+            const bool gone = cut && ((lane ^ (lane >> 3) ^ i) & 4);  // chunks 4 to 7 (i < 4: its bit 2 is 0)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(qA, (lds_ptr_t)(st + C::OFF_A + (wave * C::IPW + i) * 1024), 16,
-                                                     voA[i], so, 0, 0);
+                                                     gone ? -1 : voA[i], so, 0, 0);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(qB, (lds_ptr_t)(st + C::OFF_B + (wave * C::IPW + i) * 1024),
-                                                     16, voB[i], so, 0, 0);
+                                                     16, gone ? -1 : voB[i], so, 0, 0);
         }
         if (part != 0) return;
 #pragma unroll
         for (int j = 0; j < C::SPW; ++j) {
             const int d0 = (wave * C::SPW + j) * 64 - C::SB / 4;  // wave-uniform
             const bool su = GATED && d0 >= C::SB / 8;
+            const int vo = cut && (lane % (C::SPR / 4)) ? -1 : voS[j];
             if (d0 >= 0)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(!real ? rZ : su ? rSU : rSB, (lds_ptr_t)(st + (wave * C::SPW + j) * 256),
-                                                         4, voS[j], ss, 0, 0);
+                                                         4, vo, ss, 0, 0);
             else
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(qSA, (lds_ptr_t)(st + (wave * C::SPW + j) * 256),
-                                                         4, voS[j], ss, 0, 0);
+                                                         4, vo, ss, 0, 0);
         }
     };
     auto issue = [&](int kt) {
@@ -504,7 +510,8 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint
     constexpr int BST = GATED ? C::TN / 2 : 32;  // rows from tile 0's scales to tile 1's
     const int sshift = 8 * fg;
 
-    issue(0);
+#pragma unroll
+    for (int s = 0; s < C::NST - 1; ++s) issue(s);
 
     auto frag = [&](const uint8_t* p0, const uint8_t* p1) -> v8i {
         const u32x4 x0 = *reinterpret_cast<const u32x4*>(p0);
@@ -577,15 +584,15 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint
         for (int s = 0; s < C::NST; ++s) {
             const int kt = k0 + s;
             if (kt < KT) {
-                wait_vm<0>();    // this wave's copies of stage kt have landed
-                barrier_only();  // ... and everyone's; stage kt-1 is no longer read
-                compute(smem + s * C::STAGE, kt + 1);
+                wait_vm<(C::NST - 2) * C::LOADS>();  // this wave's copies of stage kt have landed
+                barrier_only();                      // ... and everyone's; stage kt-1 is no longer read
+                compute(smem + s * C::STAGE, kt + C::NST - 1);
             }
         }
     }
-    wait_vm<0>();  // the dummy stage's zero-fill has landed before the LDS is reused
+    wait_vm<0>();  // the dummy stages' zero-fill has landed before the LDS is reused
 
-    if constexpr (GATED) gated_epilogue<FP8, OUT, FQ, TS>(g, acc, m0, n0, smem);
+    if constexpr (GATED) gated_epilogue<FP8, OUT, FQ, TS, NS>(g, acc, m0, n0, smem);
     else big_epilogue<FP8, OUT, NVG, FQ, TS>(g, acc, m0, n0, smem);
 }
 

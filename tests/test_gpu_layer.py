@@ -371,7 +371,7 @@ def check_gated(layer, fp4, aq, gq, uq, act, dtype, **kw):
 
 
 # rows / columns / depth around the kernels' tiles: single rows, 32 and 64 rows, ragged, K of 32, off the tiles' 256
-GATED_SHAPES = [(1, 32, 32), (1, 128, 4096), (3, 100, 96), (17, 64, 256), (32, 96, 512), (33, 160, 1024), (64, 256, 768), (65, 128, 512),
+GATED_SHAPES = [(300, 200, 128), (130, 260, 384), (1, 40, 640), (50, 96, 896), (1, 32, 32), (1, 128, 4096), (3, 100, 96), (17, 64, 256), (32, 96, 512), (33, 160, 1024), (64, 256, 768), (65, 128, 512),
                 (70, 40, 256), (129, 200, 768), (200, 512, 288), (256, 384, 256), (300, 1000, 512), (513, 130, 1280)]
 
 
@@ -388,9 +388,10 @@ def test_gated(fp4, layer, m, f, k, kind):
 
 def test_gated_large_tiles(fp4, layer):
     """A grid that takes the tiles of 256 rows, ragged on both sides, all three operand kinds."""
-    for elem, tile, m, f in ((0, False, 1100, 3300), (0, True, 1030, 4096), (1, False, 1025, 3302)):
-        g = gen(m)
-        aq, gq, uq = operands(fp4, g, m, f, 256, elem, tile)
+    for elem, tile, m, f, k in ((0, False, 1100, 3300, 256), (0, True, 1030, 4096, 256), (1, False, 1025, 3302, 256),
+                                (0, False, 1500, 3200, 384), (0, True, 1030, 4096, 640)):
+        g = gen(m + k)
+        aq, gq, uq = operands(fp4, g, m, f, k, elem, tile)
         w = layer.GatedWeights(gq, uq, act=layer.SILU)
         a, wg, wu = (torch.from_numpy(plain(fp4, q)).cuda() for q in (aq, gq, uq))
         gv, uv = a @ wg.T, a @ wu.T
