@@ -163,13 +163,13 @@ __device__ __forceinline__ void gated_epilogue(const GemmArgs& g, v16f (&acc)[Bi
     if (g.h32) store_staged<DT_F32, DT_F32, C::TM, COLS, C::NTH>(smem, EP, reinterpret_cast<char*>(g.h32), g.N, m0, n0, g.M, g.N);
 }
 
-template <bool FP8, bool B2D, int OUT, int FQ, int TS, int NS>
+template <bool FP8, bool B2D, int OUT, int FQ, int TS, int NS, bool RAG>
 __global__ __launch_bounds__(TS == 256 ? 512 : 256, TS == 256 || NS > 2 ? 1 : 2) void k_gated_tile(GemmArgs g) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int ntm = (int)((g.M + TS - 1) / TS), ntn = (int)((g.N + TS / 2 - 1) / (TS / 2));
     int tm, tn;
     big_tile_coords(blockIdx.x, ntm, ntn, tm, tn);
-    big_tile<FP8, B2D, OUT, false, FQ, TS, true, NS>(g, tm, tn, smem);
+    big_tile<FP8, B2D, OUT, false, FQ, TS, true, NS, RAG>(g, tm, tn, smem);
 }
 
 // Store one place's values: gu, h, and h for a quantize pass of its own.
@@ -525,15 +525,15 @@ hipError_t plan_gated(int64_t M, int64_t F, int64_t K, bool fp8, const fp4_qpara
     p->kernel = GATED_ROWS;
     if (direct && K % 128 == 0 && M <= 64) {
         p->kernel = GATED_STREAM;
-    } else if (direct && K % 128 == 0 && ((M + 127) / 128) * ((F + 63) / 64) <= kMaxGrid) {
+    } else if (direct && M > (K % 128 ? 32 : 64) && ((M + 127) / 128) * ((F + 63) / 64) <= kMaxGrid) {
         int cus = 0;
         const hipError_t e = cu_count(&cus);
         if (e != hipSuccess) return e;
         const int64_t big = ((M + 255) / 256) * ((F + 127) / 128);
         const bool mid = M < 256 || F < 128 || 2 * big <= cus;
         const bool deep = ((M + 127) / 128) * ((F + 63) / 64) <= cus;
-        p->kernel = mid ? (deep ? GATED_TILE128_DEEP : GATED_TILE128) : GATED_TILE256;
-        columns = mid ? 64 : 128;
+        p->kernel = K % 128 ? GATED_TILE128_RAGGED : !mid ? GATED_TILE256 : deep ? GATED_TILE128_DEEP : GATED_TILE128;
+        columns = p->kernel == GATED_TILE256 ? 128 : 64;
     }
     p->quant_pass = q && (q->round_mode == FP4_ROUND_SR || q->hadamard_n > columns);
     p->ws = p->quant_pass ? M * F * 4 : 0;
@@ -566,14 +566,14 @@ static hipError_t launch_stream_m(const GemmArgs& g, hipStream_t s) {
     return launch_stream<FP8, OUT, FQ, NL, 4, 1>(g, s);
 }
 
-template <bool FP8, bool B2D, int OUT, int FQ, int TS, int NS>
+template <bool FP8, bool B2D, int OUT, int FQ, int TS, int NS, bool RAG = false>
 static hipError_t launch_tile(const GemmArgs& g, hipStream_t s) {
     using C = Big<FP8, TS, NS>;
     const size_t lds = (size_t)C::NST * C::STAGE;
-    const hipError_t e = allow_lds<k_gated_tile<FP8, B2D, OUT, FQ, TS, NS>>(lds);
+    const hipError_t e = allow_lds<k_gated_tile<FP8, B2D, OUT, FQ, TS, NS, RAG>>(lds);
     if (e != hipSuccess) return e;
     const unsigned tiles = (unsigned)(((g.M + TS - 1) / TS) * ((g.N + TS / 2 - 1) / (TS / 2)));
-    hipLaunchKernelGGL((k_gated_tile<FP8, B2D, OUT, FQ, TS, NS>), dim3(tiles), dim3(C::NTH), lds, s, g);
+    hipLaunchKernelGGL((k_gated_tile<FP8, B2D, OUT, FQ, TS, NS, RAG>), dim3(tiles), dim3(C::NTH), lds, s, g);
     return hipGetLastError();
 }
 
@@ -581,6 +581,7 @@ template <bool FP8, bool B2D, int OUT, int FQ>
 static hipError_t launch_gated_k(const GemmArgs& g, int kernel, hipStream_t s) {
     if (kernel == GATED_TILE256) return launch_tile<FP8, B2D, OUT, FQ, 256, 2>(g, s);
     if (kernel == GATED_TILE128) return launch_tile<FP8, B2D, OUT, FQ, 128, 2>(g, s);
+    if (kernel == GATED_TILE128_RAGGED) return launch_tile<FP8, B2D, OUT, FQ, 128, 2, true>(g, s);
     if (kernel == GATED_TILE128_DEEP) return launch_tile<FP8, B2D, OUT, FQ, 128, 4>(g, s);
     if (kernel == GATED_STREAM) return launch_stream_m<FP8, OUT, FQ>(g, s);
     const int64_t tiles = ((g.N + 31) / 32) * ((g.M + 31) / 32);

@@ -380,7 +380,11 @@ __device__ __forceinline__ void gated_epilogue(const GemmArgs& g, v16f (&acc)[Bi
 // GATED: two products of TS x TS / 2 results with the operands b and b_up, N columns each. The rows of B's
 // slab alternate between the two in groups of 32 (wave column wn: 32 rows of b, then the same 32 of b_up),
 // so that a lane's accumulators of tile 0 and tile 1 are the two products' values of the same place.
-template <bool FP8, bool B2D, int OUT, bool NVG, int FQ, int TS = 256, bool GATED = false, int NS = 2>
+// K is a multiple of a stage's depth; GATED also takes rows whose codes end within the last stage (K a multiple of
+// 128). RAG (GATED, two stages): K any multiple of 32. Scale rows then begin at any byte, which the copies into LDS
+// do not take: each thread reads its scale bytes of the next stage into registers and stores them when the present
+// one has been multiplied.
+template <bool FP8, bool B2D, int OUT, bool NVG, int FQ, int TS = 256, bool GATED = false, int NS = 2, bool RAG = false>
 __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint8_t* smem) {
     using C = Big<FP8, TS, NS>;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -391,7 +395,7 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint
 
     const int64_t rowbytes = FP8 ? g.K : g.K / 2;
     const int64_t kgroups = g.K / 32;
-    // K is a multiple of a stage's depth; GATED also takes E2M1 rows that end halfway through the last stage
+    static_assert(!RAG || (GATED && NS == 2), "scales through registers");
     const int KT = GATED ? (int)((g.K + C::KSTEP - 1) / C::KSTEP) : (int)(g.K / C::KSTEP);
     const bool ragged = GATED && g.K % C::KSTEP != 0;
 
@@ -453,18 +457,19 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint
         const int so = real ? kt * C::RB : 0, ss = real ? kt * C::SPR : 0;
         const __amdgpu_buffer_rsrc_t qA = real ? rA : rZ, qB = real ? rB : rZ;
         const __amdgpu_buffer_rsrc_t qSA = real ? rSA : rZ;
-        const bool cut = ragged && kt == KT - 1;  // its upper half is not there: offsets past the extent
+        const bool cut = ragged && kt == KT - 1;  // chunks past the row's end: offsets past the extent
+        const int left = (int)rowbytes - kt * C::RB;
         constexpr int IPP = C::IPW / C::NKK;
 #pragma unroll
         for (int ii = 0; ii < IPP; ++ii) {
             const int i = part * IPP + ii;
-            const bool gone = cut && ((lane ^ (lane >> 3) ^ i) & 4);  // chunks 4 to 7 (i < 4: its bit 2 is 0)
+            const bool gone = cut && 16 * ((lane & 7) ^ ((lane >> 3) & 7) ^ (i & 1)) >= left;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(qA, (lds_ptr_t)(st + C::OFF_A + (wave * C::IPW + i) * 1024), 16,
                                                      gone ? -1 : voA[i], so, 0, 0);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(qB, (lds_ptr_t)(st + C::OFF_B + (wave * C::IPW + i) * 1024),
                                                      16, gone ? -1 : voB[i], so, 0, 0);
         }
-        if (part != 0) return;
+        if (part != 0 || RAG) return;
 #pragma unroll
         for (int j = 0; j < C::SPW; ++j) {
             const int d0 = (wave * C::SPW + j) * 64 - C::SB / 4;  // wave-uniform
@@ -477,6 +482,28 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(qSA, (lds_ptr_t)(st + (wave * C::SPW + j) * 256),
                                                          4, vo, ss, 0, 0);
         }
+    };
+    // RAG: the scale dwords that the copies would place, a byte at a time (groups past the row's end: 0)
+    uint32_t held[C::SPW];
+    auto read_scales = [&](int kt) {
+#pragma unroll
+        for (int j = 0; j < C::SPW; ++j) {
+            const int d0 = (wave * C::SPW + j) * 64 - C::SB / 4;  // wave-uniform
+            const __amdgpu_buffer_rsrc_t r = kt >= KT ? rZ : d0 < 0 ? rSA : d0 >= C::SB / 8 ? rSU : rSB;
+            const int first = kt * C::SPR + 4 * (lane % (C::SPR / 4));
+            held[j] = 0u;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int vo = first + b < kgroups ? voS[j] + kt * C::SPR + b : -1;
+                held[j] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(r, vo, 0, 0) << (8 * b);
+            }
+        }
+    };
+    auto place_scales = [&](int kt) {
+        uint8_t* st = smem + (kt % C::NST) * C::STAGE;
+#pragma unroll
+        for (int j = 0; j < C::SPW; ++j)
+            *reinterpret_cast<uint32_t*>(st + (wave * C::SPW + j) * 256 + 4 * lane) = held[j];
     };
     auto issue = [&](int kt) {
 #pragma unroll
@@ -512,6 +539,10 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint
 
 #pragma unroll
     for (int s = 0; s < C::NST - 1; ++s) issue(s);
+    if constexpr (RAG) {
+        read_scales(0);
+        place_scales(0);
+    }
 
     auto frag = [&](const uint8_t* p0, const uint8_t* p1) -> v8i {
         const u32x4 x0 = *reinterpret_cast<const u32x4*>(p0);
@@ -585,8 +616,12 @@ __device__ __forceinline__ void big_tile(const GemmArgs& g, int tm, int tn, uint
             const int kt = k0 + s;
             if (kt < KT) {
                 wait_vm<(C::NST - 2) * C::LOADS>();  // this wave's copies of stage kt have landed
+                if constexpr (RAG) wait_lgkm0();     // and its scales
                 barrier_only();                      // ... and everyone's; stage kt-1 is no longer read
+                if constexpr (RAG) read_scales(kt + 1);  // (past the last stage: nothing)
                 compute(smem + s * C::STAGE, kt + C::NST - 1);
+                // not past the last stage: no write may be under way when the epilogue takes the LDS
+                if (RAG && kt + 1 < KT) place_scales(kt + 1);
             }
         }
     }

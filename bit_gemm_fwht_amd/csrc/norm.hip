@@ -283,7 +283,7 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
             for (int j = 0; j < 8; ++j) {
                 o[j] = __builtin_fmaf(rstd, dv[j] * wv[j] - sv[j] * c, base[j]);
                 // (a row that is not there was read as another one)
-                dw[i][j] = __builtin_fmaf(in ? dv[j] : 0.0f, sv[j] * rstd, dw[i][j]);
+                dw[i][j] = in ? __builtin_fmaf(dv[j], sv[j] * rstd, dw[i][j]) : dw[i][j];
             }
             if (here) piece_store<IN>(a.dx, row * a.lddx + 8 * p, piece_pack<IN>(o));
         }

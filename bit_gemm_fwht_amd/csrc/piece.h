@@ -186,7 +186,8 @@ __device__ __forceinline__ void act_slope(float g, int act, float& a, float& d) 
     } else {
         const float p = sigmoidf(2.0f * kSqrt2OverPi * (g + kGeluCubic * g * g * g));
         a = g * p;
-        d = p + g * p * (1.0f - p) * (2.0f * kSqrt2OverPi) * (1.0f + 3.0f * kGeluCubic * g * g);
+        // (the square held finite: it meets a factor of 0 where it would not be)
+        d = p + g * p * (1.0f - p) * (2.0f * kSqrt2OverPi) * (1.0f + 3.0f * kGeluCubic * fminf(g * g, 1e37f));
     }
 }
 

@@ -205,6 +205,17 @@ def test_norm_backward_against_differences(layer):
         assert abs(num - ana) <= 400 * E24 * (np.abs(f64(dx) * d).sum() + np.abs(f64(dw) * e).sum())
 
 
+def test_norm_backward_without_eps(layer):
+    """Rows that do not fill the last workgroup add nothing to the weight's gradient, whatever 1 / 0 makes of them."""
+    for rows, cols in ((5, 64), (1, 8), (130, 128), (3, 520)):
+        s, dy = rand(gen(rows), rows, cols), rand(gen(cols), rows, cols)
+        dx, dw = layer.rmsnorm_backward(dy, s, eps=0.0)
+        want, want_w = ref.rmsnorm_grad(f64(dy), f64(s), 1.0, 0.0)
+        n = f64(s) / np.sqrt((f64(s) ** 2).mean(1, keepdims=True))
+        within(dx, want, (2 * DEPTH + 16) * E24 * (np.abs(f64(dy)) + np.abs(n) * np.abs(f64(dy) * n).mean(1, keepdims=True)) / np.abs(f64(s) / n))
+        within(dw, want_w, (4 + 3 + 128 + DEPTH) * E24 * np.abs(f64(dy) * n).sum(0))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_norm_backward_in_place_and_pitches(layer, dtype):
     g = gen(9)
@@ -371,7 +382,7 @@ def check_gated(layer, fp4, aq, gq, uq, act, dtype, **kw):
 
 
 # rows / columns / depth around the kernels' tiles: single rows, 32 and 64 rows, ragged, K of 32, off the tiles' 256
-GATED_SHAPES = [(300, 200, 128), (130, 260, 384), (1, 40, 640), (50, 96, 896), (1, 32, 32), (1, 128, 4096), (3, 100, 96), (17, 64, 256), (32, 96, 512), (33, 160, 1024), (64, 256, 768), (65, 128, 512),
+GATED_SHAPES = [(100, 70, 32), (200, 96, 288), (150, 500, 1120), (300, 200, 128), (130, 260, 384), (1, 40, 640), (50, 96, 896), (1, 32, 32), (1, 128, 4096), (3, 100, 96), (17, 64, 256), (32, 96, 512), (33, 160, 1024), (64, 256, 768), (65, 128, 512),
                 (70, 40, 256), (129, 200, 768), (200, 512, 288), (256, 384, 256), (300, 1000, 512), (513, 130, 1280)]
 
 
@@ -389,7 +400,8 @@ def test_gated(fp4, layer, m, f, k, kind):
 def test_gated_large_tiles(fp4, layer):
     """A grid that takes the tiles of 256 rows, ragged on both sides, all three operand kinds."""
     for elem, tile, m, f, k in ((0, False, 1100, 3300, 256), (0, True, 1030, 4096, 256), (1, False, 1025, 3302, 256),
-                                (0, False, 1500, 3200, 384), (0, True, 1030, 4096, 640)):
+                                (0, False, 1500, 3200, 384), (0, True, 1030, 4096, 640), (0, False, 1100, 1500, 352),
+                                (1, False, 1100, 1500, 352), (0, True, 1030, 1504, 992)):
         g = gen(m + k)
         aq, gq, uq = operands(fp4, g, m, f, k, elem, tile)
         w = layer.GatedWeights(gq, uq, act=layer.SILU)
@@ -462,6 +474,14 @@ def test_gated_backward(layer, rows, f, act):
         o = pitched(gu, 16)
         assert torch.equal(layer.gated_backward(pitched(dh, 8), pitched(gu, 24), act=act, out=o).dgu, got.dgu)
         assert (o._base[:, 2 * f:] == 7).all()
+
+
+def test_gated_backward_far_from_zero(layer):
+    """Where the activation is x or 0 its slope is 1 or 0, up to the largest values."""
+    g = torch.tensor([[1e4, -1e4, 1e10, -1e10, 3e19, -3e19, 3e38, -3e38]], device="cuda")
+    for act in (0, 1, 2):
+        got = layer.gated_backward(torch.ones(1, 8, device="cuda"), torch.cat([g, torch.ones_like(g)], 1), act=act).dgu
+        assert torch.equal(got[:, :8], (g > 0).float()) and torch.equal(got[:, 8:], g.clamp(min=0))
 
 
 def test_gated_backward_against_differences(layer):
