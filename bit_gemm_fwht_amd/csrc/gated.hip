@@ -6,8 +6,8 @@
 //  - k_gated_tile: the pipelined GEMM tile (gemm_tile.h) on B slabs that hold 32 rows of Wg and the same 32
 //    of Wu in turn: 256 x 128 or 128 x 64 results a workgroup;
 //  - k_gated_stream: up to 64 rows of A, K a multiple of 128: bound by the weights' bytes;
-//  - k_gated_rows: every other K: 32 columns a workgroup, its waves each multiply a share of K straight from
-//    memory, the shares are added through LDS in a fixed order.
+//  - k_gated_rows: what neither takes (few rows of any K, operands past 2 GiB): 32 columns a workgroup, its waves
+//    each multiply a share of K straight from memory, the shares are added through LDS in a fixed order.
 #include "device.h"
 #include "fp4_internal.h"
 #include "gemm_tile.h"
@@ -388,7 +388,7 @@ __global__ __launch_bounds__(64 * NW) void k_gated_stream(GemmArgs g) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Few rows: 32 rows of A by 32 columns of h a workgroup of 8 waves. K is cut into units of 128 bytes of a row
+// Any shape: 32 rows of A by 32 columns of h a workgroup of 8 waves. K is cut into units of 128 bytes of a row
 // (256 E2M1 or 128 E4M3 values); wave w takes the units w, w + 8, .. and multiplies them with 32x32x64 scaled
 // products whose operands come straight from memory, a lane's 16 bytes at a time (lane l: row l % 32, as in
 // the tiles). Rows past the last are those of the last (their results are not stored); bytes past a row's end
@@ -518,6 +518,15 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_gated_rows(GemmArgs g) {
 // ---------------------------------------------------------------------------------------------
 // Launch
 // ---------------------------------------------------------------------------------------------
+// Which kernel, by the rows of A and the tiles that they give (times: F 11008, K 4096, 4 bits, bf16 h):
+//  - up to 64 rows: k_gated_stream (64 rows 15.9 us, tiles 15.3 at 65; 8 bits 33 and 37);
+//  - tiles of 256 rows from 256 rows on, where they fill more than half the CUs (300 rows 35.5 us, tiles of 128 rows
+//    42; 4096 rows 242 and 398), else tiles of 128 rows;
+//  - of those four stages deep where each tile has a CU to itself (65 rows 15.3 us, two stages and two workgroups a
+//    CU 19.0; 200 rows, where it has not, 28.7 and 25.0);
+//  - K off the multiples of 128: tiles of 128 rows with scales through registers, up to 32 rows k_gated_rows (K
+//    2080: 64 rows 20.3 us, tiles 16.3);
+//  - operands of 2 GiB and more, whose places leave 32 bits: k_gated_rows.
 hipError_t plan_gated(int64_t M, int64_t F, int64_t K, bool fp8, const fp4_qparams* q, GatedPlan* p) {
     const int64_t rowb = fp8 ? K : K / 2;
     const bool direct = M * rowb < (1ll << 31) && F * rowb < (1ll << 31);
@@ -550,20 +559,30 @@ static hipError_t launch_stream(const GemmArgs& g, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <bool FP8, int OUT, int FQ, int NC, int MT>
+static hipError_t launch_stream_d(const GemmArgs& g, hipStream_t s) {
+    // two buffers where a wave has eight units or more to go through (one row, 8 bits, K 4096: 23.3 us against 24.5;
+    // 4 bits, K 8192: 18.7 against 19.3), else one, which leaves room for more workgroups (4 bits, K 4096: 9.9
+    // against 10.2). With more than 32 rows two buffers leave room for one workgroup a CU alone: only where F gives no
+    // more than that (48 rows, 4 bits, K 8192, F 11008: 31.0 us with one, 33.6 with two)
+    const bool deep = (FP8 ? g.K / 128 : g.K / 256) >= 8 * kStreamWaves && (MT <= 2 || g.N <= 256 * 16 * NC);
+    return deep ? launch_stream<FP8, OUT, FQ, NC, MT, 2>(g, s) : launch_stream<FP8, OUT, FQ, NC, MT, 1>(g, s);
+}
+
 template <bool FP8, int OUT, int FQ>
 static hipError_t launch_stream_m(const GemmArgs& g, hipStream_t s) {
     // 16 columns a workgroup, so that several fit a CU and all are resident at once; 32 where groups of 32 are
-    // quantized; 48 where A's rows are most of an 8-bit unit (48 rows, K 4096, F 11008: 31.0 us, with 16 columns
-    // 32.5; in 4 bits 16.1 against 14.2)
-    constexpr int NC = FQ != FQ_NONE ? 2 : 1, NL = FQ == FQ_NONE && FP8 ? 3 : NC;
-    // two buffers where a wave has eight units or more to go through (one row, 8 bits, K 4096: 23.3 us against 24.5;
-    // 4 bits, K 8192: 18.7 against 19.3), else one, which leaves room for more workgroups (4 bits, K 4096: 9.9
-    // against 10.2)
-    const bool deep = (FP8 ? g.K / 128 : g.K / 256) >= 8 * kStreamWaves;
-    if (g.M <= 16) return deep ? launch_stream<FP8, OUT, FQ, NC, 1, 2>(g, s) : launch_stream<FP8, OUT, FQ, NC, 1, 1>(g, s);
-    if (g.M <= 32) return deep ? launch_stream<FP8, OUT, FQ, NC, 2, 2>(g, s) : launch_stream<FP8, OUT, FQ, NC, 2, 1>(g, s);
-    if (g.M <= 48) return launch_stream<FP8, OUT, FQ, NL, 3, 1>(g, s);
-    return launch_stream<FP8, OUT, FQ, NL, 4, 1>(g, s);
+    // quantized; 48 where A's rows are most of an 8-bit unit and F still gives most of the 256 CUs a workgroup (48
+    // rows, K 4096, F 11008: 24.6 us against 29.0; K 8192, F 4096: 30.6 against 19.3)
+    constexpr int NC = FQ != FQ_NONE ? 2 : 1;
+    if constexpr (FP8 && FQ == FQ_NONE) {
+        if (g.M > 32 && g.N >= 48 * 192)
+            return g.M <= 48 ? launch_stream<FP8, OUT, FQ, 3, 3, 2>(g, s) : launch_stream<FP8, OUT, FQ, 3, 4, 1>(g, s);
+    }
+    if (g.M <= 16) return launch_stream_d<FP8, OUT, FQ, NC, 1>(g, s);
+    if (g.M <= 32) return launch_stream_d<FP8, OUT, FQ, NC, 2>(g, s);
+    if (g.M <= 48) return launch_stream_d<FP8, OUT, FQ, NC, 3>(g, s);
+    return launch_stream_d<FP8, OUT, FQ, NC, 4>(g, s);
 }
 
 template <bool FP8, bool B2D, int OUT, int FQ, int TS, int NS, bool RAG = false>

@@ -307,6 +307,22 @@ int64_t fp4_gemm_gated_workspace_bytes(const fp4_qtensor* A, const fp4_qtensor* 
     }
 }
 
+int fp4_gemm_gated_plan(const fp4_qtensor* A, const fp4_qtensor* gate, const fp4_qtensor* up, const fp4_gated* o,
+                        const fp4_qparams* out_q, fp4_gated_plan* plan) {
+    try {
+        int kind, b2d;
+        GatedPlan p{};
+        if (!plan) return FP4_ERR_INVALID_ARG;
+        const int rc = check_gated(A, gate, up, o, out_q, &kind, &b2d, &p);
+        if (rc != FP4_OK) return rc;
+        plan->kernel = p.kernel;
+        plan->quantize_pass = p.quant_pass;
+        return FP4_OK;
+    } catch (...) {
+        return FP4_ERR_INTERNAL;
+    }
+}
+
 int fp4_gemm_gated(const fp4_qtensor* A, const fp4_qtensor* gate, const fp4_qtensor* up, const fp4_gated* o,
                    const fp4_qparams* out_q, fp4_qtensor* h_q, void* workspace, int64_t ws_bytes, void* stream) {
     try {

@@ -74,9 +74,9 @@ struct RopeArgs {
 hipError_t launch_rope(const RopeArgs& a, int dtype, int layout, hipStream_t s);
 
 // How a gated product is carried out: the same for the size query and the launch.
-enum { GATED_ROWS = 0, GATED_STREAM, GATED_TILE128, GATED_TILE128_DEEP, GATED_TILE128_RAGGED, GATED_TILE256 };
+enum { GATED_ROWS = 1, GATED_STREAM, GATED_TILE128, GATED_TILE128_DEEP, GATED_TILE128_RAGGED, GATED_TILE256 };
 struct GatedPlan {
-    int kernel;     // GATED_*
+    int kernel;     // GATED_*, the numbers of FP4_GATED_PLAN_*
     int quant_pass; // h goes to the workspace in fp32 and is quantized by a pass of its own
     int64_t ws;
 };

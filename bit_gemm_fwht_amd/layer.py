@@ -54,6 +54,13 @@ class GatedC(ctypes.Structure):
     _fields_ = [("h", _P), ("gu", _P), ("ldh", _I64), ("ldgu", _I64), ("dtype", _I32), ("act", _I32)]
 
 
+class GatedPlanC(ctypes.Structure):
+    _fields_ = [("kernel", _I32), ("quantize_pass", _I32)]
+
+
+PLAN_ROWS, PLAN_STREAM, PLAN_TILE128, PLAN_TILE128_DEEP, PLAN_TILE128_RAGGED, PLAN_TILE256 = range(1, 7)
+
+
 class GatedGradC(ctypes.Structure):
     _fields_ = [("dh", _P), ("gu", _P), ("dgu", _P), ("rows", _I64), ("cols", _I64), ("lddh", _I64), ("ldgu", _I64),
                 ("lddgu", _I64), ("dtype", _I32), ("act", _I32)]
@@ -71,6 +78,7 @@ def lib() -> ctypes.CDLL:
                                 ("fp4_rmsnorm_backward", [_P, _P, _I64, _P], ctypes.c_int),
                                 ("fp4_rope", [_P, _P], ctypes.c_int),
                                 ("fp4_gemm_gated_workspace_bytes", [_P, _P, _P, _P, _P], _I64),
+                                ("fp4_gemm_gated_plan", [_P, _P, _P, _P, _P, _P], ctypes.c_int),
                                 ("fp4_gemm_gated", [_P, _P, _P, _P, _P, _P, _P, _I64, _P], ctypes.c_int),
                                 ("fp4_gated_backward", [_P, _P, _P, _P], ctypes.c_int)):
             f = getattr(L, name)
@@ -80,7 +88,14 @@ def lib() -> ctypes.CDLL:
 
 
 _CODES = kv._CODES
-_code, _stream, _check = kv._code, kv._stream, kv._check
+_code, _check = kv._code, kv._check
+
+
+def _stream_of(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_stream = kv._raw_stream or _stream_of  # the current stream's handle by device index
 
 
 # Small calls last as long as their host side, so a check first asks, in as few calls as there are, whether all is
@@ -107,14 +122,15 @@ def _refuse(t: torch.Tensor, shape, dtype, index: int, name: str):
 
 def _first(t: torch.Tensor, name: str):
     """Shape, dtype code, device index and pitch of the matrix that the others of a call are held to."""
-    code = _CODES.get(t.dtype)
-    if code is None:
-        _code(t.dtype, name)
-    shape = t.shape
+    code, shape, index = _CODES.get(t.dtype), t.shape, t.get_device()
+    if code is not None and len(shape) == 2 and index >= 0:
+        ld, step = t.stride()
+        if step == 1 or shape[1] <= 1:
+            return shape, code, index, ld if shape[0] > 1 else shape[1]
+    _code(t.dtype, name)
     if len(shape) != 2:
         raise ValueError(f"{name} must be [rows, cols], not {list(shape)}")
-    index = t.get_device()
-    return shape, code, index, _matrix(t, shape, t.dtype, index, name)
+    _refuse(t, shape, t.dtype, index, name)
 
 
 def _vector(t: torch.Tensor, n: int, index: int, name: str) -> None:
@@ -150,13 +166,16 @@ def _there(index: int, call, *args, **kw):
 def _codes(q: QTensor, rows: int, cols: int, params: Params, index: int, name: str) -> None:
     """Check that q's buffers hold a [rows, cols] tensor with one scale a block (of E8M0, the only ones here)."""
     n = rows * cols
-    b = params.block
-    for t, need, what in ((q.codes, n >> 1 if params.elem == fp4.E2M1 else n, "codes"),
-                          (q.scales, n // (b[0] * b[1]), "scales")):
-        if t.get_device() != index:
-            raise ValueError(f"{name}.{what} is on {t.device}, not on cuda:{index}")
-        if not t.is_contiguous() or t.numel() * t.element_size() < need:
-            raise ValueError(f"{name}.{what} must be contiguous and hold at least {need} bytes")
+    br, bc = params.block
+    _bytes(q.codes, n >> 1 if params.elem == fp4.E2M1 else n, index, name)
+    _bytes(q.scales, n // (br * bc), index, name)
+
+
+def _bytes(t: torch.Tensor, need: int, index: int, name: str) -> None:
+    if t.get_device() != index:
+        raise ValueError(f"a buffer of {name} is on {t.device}, not on cuda:{index}")
+    if t.nbytes < need or not t.is_contiguous():
+        raise ValueError(f"a buffer of {name} must be contiguous and hold at least {need} bytes")
 
 
 def _quant_out(rows: int, cols: int, params: Params, dev, index: int, q_out) -> QTensor:
@@ -233,7 +252,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e
         qa = ctypes.addressof(qc)
     elif q_out is not None:
         raise ValueError("q_out goes with out_q")
-    st = lib().fp4_rmsnorm(ctypes.addressof(c), qp, qa, _stream(dev))
+    st = lib().fp4_rmsnorm(ctypes.addressof(c), qp, qa, _stream(index))
     if st:
         _check(st, "fp4_rmsnorm")
     if q_out is not None:
@@ -280,7 +299,7 @@ def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor | N
     if need > 0:
         workspace = _workspace(workspace, need, dev)
         ws = workspace.data_ptr()
-    st = L.fp4_rmsnorm_backward(pc, ws, need, _stream(dev))
+    st = L.fp4_rmsnorm_backward(pc, ws, need, _stream(index))
     if st:
         _check(st, "fp4_rmsnorm_backward")
     return out, dweight
@@ -399,7 +418,7 @@ def rope(x, rotary: Rotary, positions, out=None, backward: bool = False):
         x1_ld = x1_head = o1_ld = o1_head = 0
     c = RopeC(a.data_ptr(), x1, o.data_ptr(), y1, x_ld, x1_ld, x_head, x1_head, o_ld, o1_ld, o_head, o1_head, heads, heads_b, tokens,
               rotary._ptr, pos, batch, rotary.scale, code, dim, rotary.rotary_dim, rotary.layout, backward)
-    st = lib().fp4_rope(ctypes.addressof(c), _stream(dev))
+    st = lib().fp4_rope(ctypes.addressof(c), _stream(index))
     if st:
         _check(st, "fp4_rope")
     return (o, p) if pair else o
@@ -503,12 +522,28 @@ def gated(a: QTensor, weights: GatedWeights, out_dtype=torch.bfloat16, out: torc
             ws = workspace.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out goes with out_q")
-    st = L.fp4_gemm_gated(pa, pg, pu, po, qp, qa, ws, need, _stream(dev))
+    st = L.fp4_gemm_gated(pa, pg, pu, po, qp, qa, ws, need, _stream(index))
     if st:
         _check(st, "fp4_gemm_gated")
     if q_out is not None:
         _describe(q_out, rows, ff, out_q)
     return Gated(out, q_out, gu)
+
+
+def gated_plan(rows: int, weights: GatedWeights, dtype=torch.bfloat16, out_q: Params | None = None) -> GatedPlanC:
+    """How gated() of a [rows, K] would be carried out: kernel (PLAN_...), quantize_pass."""
+    p = weights.gate.params
+    ac = fp4.QTensorC(None, None, None, rows, weights.hidden, Params(elem=p.elem, hadamard_n=p.hadamard_n).c())
+    c, plan = GatedC(dtype=_code(dtype, "out"), act=weights.act), GatedPlanC()
+    _check(lib().fp4_gemm_gated_plan(ctypes.addressof(ac), *weights._p, ctypes.addressof(c),
+                                     None if out_q is None else ctypes.addressof(_params_c(out_q)), ctypes.addressof(plan)),
+           "fp4_gemm_gated_plan")
+    return plan
+
+
+def gated_workspace_bytes(rows: int, weights: GatedWeights, out_q: Params) -> int:
+    """Bytes of workspace gated() of a [rows, K] with out_q needs."""
+    return 4 * rows * weights.ff if gated_plan(rows, weights, out_q=out_q).quantize_pass else 0
 
 
 class GatedGrad(NamedTuple):
@@ -542,7 +577,7 @@ def gated_backward(dh: torch.Tensor, gu: torch.Tensor, act: int = SILU, out: tor
         qa = ctypes.addressof(qc)
     elif q_out is not None:
         raise ValueError("q_out goes with out_q")
-    st = lib().fp4_gated_backward(ctypes.addressof(c), qp, qa, _stream(dev))
+    st = lib().fp4_gated_backward(ctypes.addressof(c), qp, qa, _stream(index))
     if st:
         _check(st, "fp4_gated_backward")
     if q_out is not None:
@@ -552,4 +587,4 @@ def gated_backward(dh: torch.Tensor, gu: torch.Tensor, act: int = SILU, out: tor
 
 __all__ = ["SILU", "GELU", "GELU_TANH", "HALF", "INTERLEAVED", "Normed", "Gated", "GatedGrad", "GatedWeights", "Rotary",
            "rmsnorm", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes", "rotary_frequencies", "rope", "gated",
-           "gated_backward"]
+           "gated_plan", "gated_workspace_bytes", "gated_backward"]

@@ -505,8 +505,8 @@ int fp4_rope(const fp4_rope_args* a, void* stream);
  * Phi(x) ~ (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2.
  * How the work is tiled changes the order of the sums, never what is meant. workspace:
  * fp4_gemm_gated_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0; -1 for arguments that the
- * call would reject; only M, F, K, the parameters, dtype and out_q matter): h in fp32 where a rotation spans
- * more columns than a tile. */
+ * call would reject; only M, F, K, the parameters, dtype and out_q matter; 0 without out_q): h in fp32 where a
+ * rotation spans more columns than a workgroup has, and for stochastic rounding. */
 enum { FP4_ACT_SILU = 0, FP4_ACT_GELU = 1, FP4_ACT_GELU_TANH = 2 };
 typedef struct fp4_gated {
     void* h;
@@ -517,6 +517,22 @@ typedef struct fp4_gated {
 } fp4_gated;
 int64_t fp4_gemm_gated_workspace_bytes(const fp4_qtensor* A, const fp4_qtensor* gate, const fp4_qtensor* up,
                                        const fp4_gated* o, const fp4_qparams* out_q);
+/* How the call would be carried out, for profiles and tests: which kernel, and whether h is quantized by a launch of
+ * its own. A choice of speed alone, free to change. No rows: both zero. */
+enum {
+    FP4_GATED_PLAN_ROWS = 1,     /* 32 rows by 32 columns, operands straight from memory */
+    FP4_GATED_PLAN_STREAM = 2,   /* up to 64 rows, weights through LDS once */
+    FP4_GATED_PLAN_TILE128 = 3,  /* tiles of 128 rows by 64 columns */
+    FP4_GATED_PLAN_TILE128_DEEP = 4,   /* the same, four stages deep */
+    FP4_GATED_PLAN_TILE128_RAGGED = 5, /* the same for any K */
+    FP4_GATED_PLAN_TILE256 = 6   /* tiles of 256 rows by 128 columns */
+};
+typedef struct fp4_gated_plan {
+    int32_t kernel;
+    int32_t quantize_pass;
+} fp4_gated_plan;
+int fp4_gemm_gated_plan(const fp4_qtensor* A, const fp4_qtensor* gate, const fp4_qtensor* up, const fp4_gated* o,
+                        const fp4_qparams* out_q, fp4_gated_plan* plan);
 int fp4_gemm_gated(const fp4_qtensor* A, const fp4_qtensor* gate, const fp4_qtensor* up, const fp4_gated* o,
                    const fp4_qparams* out_q, fp4_qtensor* h_q, void* workspace, int64_t ws_bytes, void* stream);
 

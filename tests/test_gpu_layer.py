@@ -363,6 +363,10 @@ def product_bound(a, b, fp8):
     return tol
 
 
+CODED_SHAPES = [(1, 128, 512), (48, 384, 256), (100, 256, 512), (65, 128, 96), (300, 640, 512), (1030, 3328, 256), (35, 128, 4096),
+                (48, 9600, 256)]
+
+
 def check_gated(layer, fp4, aq, gq, uq, act, dtype, **kw):
     w = layer.GatedWeights(gq, uq, act=act)
     got = layer.gated(aq, w, out_dtype=dtype, keep_gu=True, **kw)
@@ -383,7 +387,8 @@ def check_gated(layer, fp4, aq, gq, uq, act, dtype, **kw):
 
 # rows / columns / depth around the kernels' tiles: single rows, 32 and 64 rows, ragged, K of 32, off the tiles' 256
 GATED_SHAPES = [(100, 70, 32), (200, 96, 288), (150, 500, 1120), (300, 200, 128), (130, 260, 384), (1, 40, 640), (50, 96, 896), (1, 32, 32), (1, 128, 4096), (3, 100, 96), (17, 64, 256), (32, 96, 512), (33, 160, 1024), (64, 256, 768), (65, 128, 512),
-                (70, 40, 256), (129, 200, 768), (200, 512, 288), (256, 384, 256), (300, 1000, 512), (513, 130, 1280)]
+                (70, 40, 256), (129, 200, 768), (200, 512, 288), (256, 384, 256), (300, 1000, 512), (513, 130, 1280),
+                (40, 9300, 128), (60, 9300, 256), (35, 64, 4096), (55, 64, 8192)]
 
 
 @pytest.mark.parametrize("kind", ["e2m1", "tile", "e4m3"])
@@ -395,6 +400,37 @@ def test_gated(fp4, layer, m, f, k, kind):
     aq, gq, uq = operands(fp4, g, m, f, k, fp4.E4M3 if kind == "e4m3" else fp4.E2M1, kind == "tile")
     for act, dtype in ((0, torch.float32), (1, torch.bfloat16), (2, torch.float32)):
         check_gated(layer, fp4, aq, gq, uq, act, dtype)
+
+
+def test_gated_shapes_reach_every_kernel(fp4, layer):
+    """The shapes of these tests go by the choice of kernel: each kernel is among them, with and without a launch of its
+    own for the codes."""
+    def plan(m, f, k, elem=0, out_q=None):
+        q = [fp4.empty_qtensor(f, k, fp4.Params(elem=elem), "cuda") for _ in range(2)]
+        p = layer.gated_plan(m, layer.GatedWeights(*q), out_q=out_q)
+        return p.kernel, p.quantize_pass
+    got = {plan(*s)[0] for s in GATED_SHAPES}
+    assert got >= {layer.PLAN_ROWS, layer.PLAN_STREAM, layer.PLAN_TILE128_DEEP, layer.PLAN_TILE128_RAGGED}
+    assert plan(1100, 3300, 256) == (layer.PLAN_TILE256, 0) and plan(600, 6000, 256) == (layer.PLAN_TILE256, 0)
+    assert plan(200, 11008, 256) == (layer.PLAN_TILE128, 0) and plan(255, 13000, 384)[0] == layer.PLAN_TILE128
+    assert plan(1100, 1500, 352)[0] == layer.PLAN_TILE128_RAGGED
+    modes = {plan(m, f, k, out_q=fp4.Params(hadamard_n=hn)) for m, f, k in CODED_SHAPES for hn in (0, 128)}
+    assert {p for _, p in modes} == {0, 1} and (layer.PLAN_TILE256, 0) in modes and (layer.PLAN_TILE128_DEEP, 1) in modes
+
+
+def test_gated_many_small_tiles(fp4, layer):
+    """More tiles of 128 rows than CUs, two workgroups on each."""
+    for elem, m, f, k in ((0, 200, 11008, 256), (0, 250, 9001, 384), (1, 131, 10000, 128)):
+        aq, gq, uq = operands(fp4, gen(m), m, f, k, elem, False)
+        w = layer.GatedWeights(gq, uq, act=layer.GELU_TANH)
+        assert layer.gated_plan(m, w).kernel == layer.PLAN_TILE128
+        got = layer.gated(aq, w, out_dtype=torch.float32, keep_gu=True)
+        a, wg, wu = (torch.from_numpy(plain(fp4, q)).cuda() for q in (aq, gq, uq))
+        part = 1e-5 + (2.0 ** -10 if elem else 0.0)
+        for y, b in ((got.gu[:, :f], wg), (got.gu[:, f:], wu)):
+            assert ((y.double() - a @ b.T).abs() <= part * (a.abs() @ b.abs().T)).all()
+        h = torch.nn.functional.gelu(got.gu[:, :f].double(), approximate="tanh") * got.gu[:, f:].double()
+        assert ((got.h.double() - h).abs() <= 2.0 ** -20 * got.gu[:, :f].double().abs() * got.gu[:, f:].double().abs()).all()
 
 
 def test_gated_large_tiles(fp4, layer):
@@ -422,7 +458,7 @@ def test_gated_large_tiles(fp4, layer):
 
 @pytest.mark.parametrize("mode", [(0, 0, 0, 0), (0, 32, 1, 0), (0, 64, 0, 0), (0, 128, 0, 0), (0, 128, 0, 1), (1, 0, 1, 0), (1, 16, 0, 1),
                                   (1, 64, 1, 0), (1, 128, 1, 0)])
-@pytest.mark.parametrize("m,f,k", [(1, 128, 512), (48, 384, 256), (100, 256, 512), (65, 128, 96), (300, 640, 512), (1030, 3328, 256)])
+@pytest.mark.parametrize("m,f,k", CODED_SHAPES)
 def test_gated_codes_are_those_of_quantize(fp4, layer, m, f, k, mode):
     g = gen(m + f)
     for elem in (0, 1):

@@ -221,6 +221,22 @@ def test_gated_quant_refusals_and_workspace(layer, fp4):
     assert (q.rows, q.cols) == (0, 512)
 
 
+def test_gated_plan(layer, fp4):
+    """Few rows, which need no device: the kernel by K, the launch of its own by the rotation and the rounding."""
+    L, plan = layer.lib(), layer.GatedPlanC()
+    for k, kernel in ((256, layer.PLAN_STREAM), (384, layer.PLAN_STREAM), (96, layer.PLAN_ROWS)):
+        a, g, u, o = gated_args(layer, fp4, f=512, k=k)
+        for kw, alone in ((None, 0), (dict(hadamard_n=32), 0), (dict(hadamard_n=64), 1), (dict(round_mode=1), 1)):
+            p = None if kw is None else quant(fp4, **kw)[0]
+            assert L.fp4_gemm_gated_plan(ptr(a), ptr(g), ptr(u), ptr(o), None if p is None else ptr(p), ptr(plan)) == fp4.OK
+            assert (plan.kernel, plan.quantize_pass) == (kernel, alone)
+            if p is not None:
+                assert L.fp4_gemm_gated_workspace_bytes(ptr(a), ptr(g), ptr(u), ptr(o), ptr(p)) == alone * 4 * 512 * 4
+    a.rows = 0
+    assert L.fp4_gemm_gated_plan(ptr(a), ptr(g), ptr(u), ptr(o), None, ptr(plan)) == fp4.OK and plan.kernel == 0
+    assert L.fp4_gemm_gated_plan(ptr(a), ptr(g), ptr(u), ptr(o), None, None) == fp4.ERR_INVALID_ARG
+
+
 def gated_grad(layer, **kw):
     a = dict(dh=0x10000, gu=0x20000, dgu=0x30000, rows=4, cols=64, lddh=64, ldgu=128, lddgu=128, dtype=1, act=0)
     a.update(kw)
