@@ -163,12 +163,26 @@ __device__ __forceinline__ void gated_epilogue(const GemmArgs& g, v16f (&acc)[Bi
     if (g.h32) store_staged<DT_F32, DT_F32, C::TM, COLS, C::NTH>(smem, EP, reinterpret_cast<char*>(g.h32), g.N, m0, n0, g.M, g.N);
 }
 
+// Tile coordinates of workgroup b: each of the 8 XCDs, which receive ids in turn, owns a run of tiles that follow one
+// another, walked in groups of 4 tile rows, so that what an XCD's CUs read at once stays in its L2 (2048 rows, K 4096, F
+// 11008: 128 us; groups of 2 138, of 16 139; without runs of their own where 8 does not divide the tiles 300 rows take
+// 39.3 us for 36.8).
+__device__ __forceinline__ void gated_tile_coords(int b, int ntm, int ntn, int& tm, int& tn) {
+    constexpr int GM = 4;
+    const int T = ntm * ntn, xcd = b % 8, each = T / 8, more = T % 8;
+    b = xcd * each + min(xcd, more) + b / 8;
+    const int grp = b / (GM * ntn), first = grp * GM;
+    const int gs = min(ntm - first, GM);
+    tm = first + (b % (GM * ntn)) % gs;
+    tn = (b % (GM * ntn)) / gs;
+}
+
 template <bool FP8, bool B2D, int OUT, int FQ, int TS, int NS, bool RAG>
 __global__ __launch_bounds__(TS == 256 ? 512 : 256, TS == 256 || NS > 2 ? 1 : 2) void k_gated_tile(GemmArgs g) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int ntm = (int)((g.M + TS - 1) / TS), ntn = (int)((g.N + TS / 2 - 1) / (TS / 2));
     int tm, tn;
-    big_tile_coords(blockIdx.x, ntm, ntn, tm, tn);
+    gated_tile_coords(blockIdx.x, ntm, ntn, tm, tn);
     big_tile<FP8, B2D, OUT, false, FQ, TS, true, NS, RAG>(g, tm, tn, smem);
 }
 
