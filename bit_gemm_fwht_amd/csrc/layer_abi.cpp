@@ -119,9 +119,11 @@ int check_gated(const fp4_qtensor* A, const fp4_qtensor* G, const fp4_qtensor* U
     return hip_status(plan_gated(M, F, K, *kind == 1, out_q, plan));
 }
 
+// scales of K a multiple of 128 are read four at a time, others one at a time (a fused weight's lower half may then
+// begin anywhere)
 int check_codes(const fp4_qtensor* t) {
     if (!t->codes || !t->scales) return FP4_ERR_INVALID_ARG;
-    if (!aligned(t->codes, 16) || !aligned(t->scales, 4)) return FP4_ERR_ALIGNMENT;
+    if (!aligned(t->codes, 16) || (t->cols % 128 == 0 && !aligned(t->scales, 4))) return FP4_ERR_ALIGNMENT;
     return FP4_OK;
 }
 

@@ -423,7 +423,9 @@ int fp4_kv_attention(const fp4_kv_cache* cache, const fp4_kv_batch* batch, const
  * What is normed is what sum holds. residual and sum: both or neither; sum may be x or residual themselves
  * (then of the same pitch), y may be x. weight [cols], of w_dtype, or NULL for ones. y may be NULL where
  * out_q is given. cols: a multiple of 8 up to 32768 (of 32, and of hadamard_n, with out_q); rows below
- * 2^31. Sums of squares that leave fp32's range are outside the contract. */
+ * 2^31. eps >= 0; a row of zeros needs eps > 0 (0 / 0 is NaN). Sums of squares that leave fp32's range are
+ * outside the contract. A row's sum is split over more lanes where there are few rows, so its last bits may
+ * depend on how many rows a call has. */
 typedef struct fp4_norm {
     const void* x;
     const void* residual;
@@ -499,8 +501,8 @@ int fp4_rope(const fp4_rope_args* a, void* stream);
  * in one pass over the operands. Operand pairs as for fp4_gemm without NVFP4: MXFP4 (the weights may use
  * (32, 32) tiles) or MXFP8; gate and up share one set of parameters, and A's rotation. h [M, F] and gu
  * [M, 2 F] (g, then u: what fp4_gated_backward reads) of dtype, either may be NULL; out_q / h_q as above with
- * hadamard_n <= 128 and F % 32 == 0; at least one of the three outputs. Pitches need not be multiples of
- * 16 bytes (that only narrows the stores).
+ * hadamard_n <= 128 and F % 32 == 0; at least one of the three outputs. Codes 16-byte aligned, scales 4-byte
+ * where K % 128 == 0. Pitches need not be multiples of 16 bytes (that only narrows the stores).
  * act: x / (1 + e^-x); x Phi(x) with the error function; the same with
  * Phi(x) ~ (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2.
  * How the work is tiled changes the order of the sums, never what is meant. workspace:

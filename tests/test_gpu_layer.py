@@ -492,6 +492,23 @@ def test_gated_fused_weights_pitches_and_rotation(fp4, layer):
             assert (o[:, f:] == 3).all() and (gu[:, 2 * f:] == 3).all()
 
 
+@pytest.mark.parametrize("m,f,k", [(1, 33, 32), (20, 35, 96), (40, 33, 96), (140, 67, 160), (300, 129, 2080)])
+def test_gated_scales_that_begin_at_any_byte(fp4, layer, m, f, k):
+    """The lower half of a fused weight, and a batch's rows, whose scales begin off a multiple of 4 bytes."""
+    g = gen(m + k)
+    for elem in (fp4.E2M1, fp4.E4M3):
+        aq, gq, uq = operands(fp4, g, m + 1, f, k, elem, False)
+        both = fp4.QTensor(torch.cat([gq.codes, uq.codes]), torch.cat([gq.scales, uq.scales]), None, 2 * f, k, gq.params)
+        cut = k if elem == fp4.E4M3 else k // 2
+        rest = fp4.QTensor(aq.codes.view(-1)[cut:], aq.scales.view(-1)[k // 32:], None, m, k, aq.params)
+        assert (f * k // 32) % 4 and (k // 32) % 4
+        same = fp4.QTensor(rest.codes.clone(), rest.scales.clone(), None, m, k, aq.params)
+        want = layer.gated(same, layer.GatedWeights(gq, uq), keep_gu=True)
+        got = layer.gated(rest, layer.GatedWeights(both), keep_gu=True)
+        assert torch.equal(got.h, want.h) and torch.equal(got.gu, want.gu)
+        assert want.gu.isfinite().all() and want.gu.abs().amax() > 0
+
+
 @pytest.mark.parametrize("act", [0, 1, 2])
 @pytest.mark.parametrize("rows,f", [(1, 8), (1, 128), (3, 104), (7, 1000), (65, 256), (33, 1376), (2, 11008)])
 def test_gated_backward(layer, rows, f, act):
