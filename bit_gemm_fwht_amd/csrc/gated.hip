@@ -532,9 +532,17 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_gated_rows(GemmArgs g) {
 // ---------------------------------------------------------------------------------------------
 // Launch
 // ---------------------------------------------------------------------------------------------
+// Workgroups of 16 columns that k_gated_stream would have: rows of A in equal parts of at most 64.
+static int64_t stream_parts(int64_t M) { return (M + 63) / 64; }
+static int64_t stream_groups(int64_t M, int64_t F) { return stream_parts(M) * ((F + 15) / 16); }
+
 // Which kernel, by the rows of A and the tiles that they give (times: F 11008, K 4096, 4 bits, bf16 h):
 //  - up to 64 rows: k_gated_stream (64 rows 15.9 us, tiles 15.3 at 65; 8 bits 33 and 37);
-//  - tiles of 256 rows from 256 rows on, where they fill more than half the CUs (300 rows 35.5 us, tiles of 128 rows
+//  - with more it reads the weights again for each 64 rows, but its waves share K, and few tiles are bound by how
+//    long one takes for K: up to 2 3/4 workgroups of 16 columns a CU (F 1376: 128 rows 7.6 us, tiles 14.8; 512 rows
+//    15.2 and 16.5, 1024 rows 24.8 and 16.9), 2 in 8 bits (F 1376: 256 rows 16.1 us and 23.8; 512 rows 25.2 and 23.9)
+//    and where it codes h, which takes 32 columns a workgroup, and 1 where it alone would need a pass to code h;
+//  - tiles of 256 rows from 256 rows on, where they fill more than half the CUs (300 rows 36.8 us, tiles of 128 rows
 //    42; 4096 rows 242 and 398), else tiles of 128 rows;
 //  - of those four stages deep where each tile has a CU to itself (65 rows 15.3 us, two stages and two workgroups a
 //    CU 19.0; 200 rows, where it has not, 28.7 and 25.0);
@@ -555,8 +563,15 @@ hipError_t plan_gated(int64_t M, int64_t F, int64_t K, bool fp8, const fp4_qpara
         const int64_t big = ((M + 255) / 256) * ((F + 127) / 128);
         const bool mid = M < 256 || F < 128 || 2 * big <= cus;
         const bool deep = ((M + 127) / 128) * ((F + 63) / 64) <= cus;
-        p->kernel = K % 128 ? GATED_TILE128_RAGGED : !mid ? GATED_TILE256 : deep ? GATED_TILE128_DEEP : GATED_TILE128;
-        columns = p->kernel == GATED_TILE256 ? 128 : 64;
+        const bool nearest = q && q->round_mode != FP4_ROUND_SR;
+        const bool alone = nearest && q->hadamard_n == 64, codes = nearest && q->hadamard_n <= 32;
+        const int quarters = alone ? 4 : fp8 || codes ? 8 : 11;
+        if (K % 128 == 0 && 4 * stream_groups(M, F) <= quarters * cus) {
+            p->kernel = GATED_STREAM;
+        } else {
+            p->kernel = K % 128 ? GATED_TILE128_RAGGED : !mid ? GATED_TILE256 : deep ? GATED_TILE128_DEEP : GATED_TILE128;
+            columns = p->kernel == GATED_TILE256 ? 128 : 64;
+        }
     }
     p->quant_pass = q && (q->round_mode == FP4_ROUND_SR || q->hadamard_n > columns);
     p->ws = p->quant_pass ? M * F * 4 : 0;
@@ -568,7 +583,7 @@ static hipError_t launch_stream(const GemmArgs& g, hipStream_t s) {
     using S = Stream<FP8, NC, MT, kStreamWaves, D>;
     const hipError_t e = allow_lds<k_gated_stream<FP8, OUT, FQ, NC, MT, kStreamWaves, D>>(S::LDS);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_gated_stream<FP8, OUT, FQ, NC, MT, kStreamWaves, D>), dim3((unsigned)((g.N + S::WR - 1) / S::WR)),
+    hipLaunchKernelGGL((k_gated_stream<FP8, OUT, FQ, NC, MT, kStreamWaves, D>), dim3((unsigned)((g.N + S::WR - 1) / S::WR), (unsigned)stream_parts(g.M)),
                        dim3(64 * kStreamWaves), S::LDS, s, g);
     return hipGetLastError();
 }
@@ -577,9 +592,11 @@ template <bool FP8, int OUT, int FQ, int NC, int MT>
 static hipError_t launch_stream_d(const GemmArgs& g, hipStream_t s) {
     // two buffers where a wave has eight units or more to go through (one row, 8 bits, K 4096: 23.3 us against 24.5;
     // 4 bits, K 8192: 18.7 against 19.3), else one, which leaves room for more workgroups (4 bits, K 4096: 9.9
-    // against 10.2). With more than 32 rows two buffers leave room for one workgroup a CU alone: only where F gives no
-    // more than that (48 rows, 4 bits, K 8192, F 11008: 31.0 us with one, 33.6 with two)
-    const bool deep = (FP8 ? g.K / 128 : g.K / 256) >= 8 * kStreamWaves && (MT <= 2 || g.N <= 256 * 16 * NC);
+    // against 10.2). With more than 32 rows two buffers leave room for one workgroup a CU alone: only where there are
+    // no more than that (48 rows, 4 bits, K 8192, F 11008: 31.0 us with one, 33.6 with two), and then for any K (128
+    // rows, K 4096, F 1376: 7.6 against 8.7)
+    const bool alone = stream_parts(g.M) * ((g.N + 16 * NC - 1) / (16 * NC)) <= 256;
+    const bool deep = alone || (MT <= 2 && (FP8 ? g.K / 128 : g.K / 256) >= 8 * kStreamWaves);
     return deep ? launch_stream<FP8, OUT, FQ, NC, MT, 2>(g, s) : launch_stream<FP8, OUT, FQ, NC, MT, 1>(g, s);
 }
 
@@ -587,15 +604,19 @@ template <bool FP8, int OUT, int FQ>
 static hipError_t launch_stream_m(const GemmArgs& g, hipStream_t s) {
     // 16 columns a workgroup, so that several fit a CU and all are resident at once; 32 where groups of 32 are
     // quantized; 48 where A's rows are most of an 8-bit unit and F still gives most of the 256 CUs a workgroup (48
-    // rows, K 4096, F 11008: 24.6 us against 29.0; K 8192, F 4096: 30.6 against 19.3)
+    // rows, K 4096, F 11008: 24.6 us against 29.0; K 8192, F 4096: 30.6 against 19.3); 32 where 8-bit workgroups for
+    // several parts of A would be more than the CUs (256 rows, K 4096, F 1376: 16.1 us against 18.2)
     constexpr int NC = FQ != FQ_NONE ? 2 : 1;
+    const int64_t rows = (g.M + stream_parts(g.M) - 1) / stream_parts(g.M);
     if constexpr (FP8 && FQ == FQ_NONE) {
-        if (g.M > 32 && g.N >= 48 * 192)
+        if (g.M <= 64 && g.M > 32 && g.N >= 48 * 192)
             return g.M <= 48 ? launch_stream<FP8, OUT, FQ, 3, 3, 2>(g, s) : launch_stream<FP8, OUT, FQ, 3, 4, 1>(g, s);
+        if (g.M > 64 && stream_groups(g.M, g.N) > 256)
+            return rows <= 48 ? launch_stream<FP8, OUT, FQ, 2, 3, 1>(g, s) : launch_stream<FP8, OUT, FQ, 2, 4, 1>(g, s);
     }
-    if (g.M <= 16) return launch_stream_d<FP8, OUT, FQ, NC, 1>(g, s);
-    if (g.M <= 32) return launch_stream_d<FP8, OUT, FQ, NC, 2>(g, s);
-    if (g.M <= 48) return launch_stream_d<FP8, OUT, FQ, NC, 3>(g, s);
+    if (rows <= 16) return launch_stream_d<FP8, OUT, FQ, NC, 1>(g, s);
+    if (rows <= 32) return launch_stream_d<FP8, OUT, FQ, NC, 2>(g, s);
+    if (rows <= 48) return launch_stream_d<FP8, OUT, FQ, NC, 3>(g, s);
     return launch_stream_d<FP8, OUT, FQ, NC, 4>(g, s);
 }
 
