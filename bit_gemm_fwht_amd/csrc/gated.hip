@@ -540,7 +540,7 @@ static int64_t stream_groups(int64_t M, int64_t F) { return stream_parts(M) * ((
 //  - up to 64 rows: k_gated_stream (64 rows 15.9 us, tiles 15.3 at 65; 8 bits 33 and 37);
 //  - with more it reads the weights again for each 64 rows, but its waves share K, and few tiles are bound by how
 //    long one takes for K: up to 2 3/4 workgroups of 16 columns a CU (F 1376: 128 rows 7.6 us, tiles 14.8; 512 rows
-//    15.2 and 16.5, 1024 rows 24.8 and 16.9), 2 in 8 bits (F 1376: 256 rows 16.1 us and 23.8; 512 rows 25.2 and 23.9)
+//    15.2 and 16.5, 1024 rows 24.8 and 16.9), 2 in 8 bits (F 1376: 256 rows 14.8 us and 23.8; 512 rows 25.2 and 23.9)
 //    and where it codes h, which takes 32 columns a workgroup, and 1 where it alone would need a pass to code h;
 //  - tiles of 256 rows from 256 rows on, where they fill more than half the CUs (300 rows 36.8 us, tiles of 128 rows
 //    42; 4096 rows 242 and 398), else tiles of 128 rows;
@@ -604,15 +604,20 @@ template <bool FP8, int OUT, int FQ>
 static hipError_t launch_stream_m(const GemmArgs& g, hipStream_t s) {
     // 16 columns a workgroup, so that several fit a CU and all are resident at once; 32 where groups of 32 are
     // quantized; 48 where A's rows are most of an 8-bit unit and F still gives most of the 256 CUs a workgroup (48
-    // rows, K 4096, F 11008: 24.6 us against 29.0; K 8192, F 4096: 30.6 against 19.3); 32 where 8-bit workgroups for
-    // several parts of A would be more than the CUs (256 rows, K 4096, F 1376: 16.1 us against 18.2)
+    // rows, K 4096, F 11008: 24.6 us against 29.0; K 8192, F 4096: 30.6 against 19.3); 32, two buffers deep, where
+    // that makes no more workgroups than CUs of what would be up to twice as many, and a wave has two units (256 rows,
+    // K 4096, F 1376: 10.7 us against 11.8, 8 bits 14.8 against 18.2; 64 rows of F 5504 10.4 and 11.5, 15.2 and 18.0;
+    // K 256, 512 rows of F 1024: 5.5 against 4.4)
     constexpr int NC = FQ != FQ_NONE ? 2 : 1;
     const int64_t rows = (g.M + stream_parts(g.M) - 1) / stream_parts(g.M);
     if constexpr (FP8 && FQ == FQ_NONE) {
         if (g.M <= 64 && g.M > 32 && g.N >= 48 * 192)
             return g.M <= 48 ? launch_stream<FP8, OUT, FQ, 3, 3, 2>(g, s) : launch_stream<FP8, OUT, FQ, 3, 4, 1>(g, s);
-        if (g.M > 64 && stream_groups(g.M, g.N) > 256)
-            return rows <= 48 ? launch_stream<FP8, OUT, FQ, 2, 3, 1>(g, s) : launch_stream<FP8, OUT, FQ, 2, 4, 1>(g, s);
+    }
+    if constexpr (FQ == FQ_NONE) {
+        const int64_t groups = stream_groups(g.M, g.N);
+        if (rows > 32 && groups > 256 && groups <= 512 && (FP8 ? g.K / 128 : g.K / 256) >= 2 * kStreamWaves)
+            return rows <= 48 ? launch_stream_d<FP8, OUT, FQ, 2, 3>(g, s) : launch_stream_d<FP8, OUT, FQ, 2, 4>(g, s);
     }
     if (rows <= 16) return launch_stream_d<FP8, OUT, FQ, NC, 1>(g, s);
     if (rows <= 32) return launch_stream_d<FP8, OUT, FQ, NC, 2>(g, s);

@@ -388,8 +388,9 @@ def check_gated(layer, fp4, aq, gq, uq, act, dtype, **kw):
 # rows / columns / depth around the kernels' tiles: single rows, 32 and 64 rows, ragged, K of 32, off the tiles' 256
 GATED_SHAPES = [(100, 70, 32), (200, 96, 288), (150, 500, 1120), (300, 200, 128), (130, 260, 384), (1, 40, 640), (50, 96, 896), (1, 32, 32), (1, 128, 4096), (3, 100, 96), (17, 64, 256), (32, 96, 512), (33, 160, 1024), (64, 256, 768), (65, 128, 512),
                 (70, 40, 256), (129, 200, 768), (200, 512, 288), (256, 384, 256), (300, 1000, 512), (513, 130, 1280),
-                (40, 9300, 128), (60, 9300, 256), (35, 64, 4096), (55, 64, 8192), (66, 6000, 512), (130, 4100, 384), (513, 1400, 1280),
-                (200, 4000, 128), (97, 1376, 512), (260, 1400, 384)]
+                (40, 9300, 128), (60, 9300, 256), (35, 64, 4096), (55, 64, 8192), (66, 6000, 512), (130, 4100, 384), (513, 1400, 256),
+                (200, 4000, 128), (97, 1376, 512), (260, 1400, 384), (115, 2064, 2048),
+                (66, 2064, 1024)]
 
 
 @pytest.mark.parametrize("kind", ["e2m1", "tile", "e4m3"])
