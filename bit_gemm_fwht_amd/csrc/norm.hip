@@ -12,9 +12,8 @@ namespace bgf {
 
 constexpr int kNormThreads = 512;  // of a workgroup at most: rows of 32768 in 8 pieces a lane
 
-// Sums of a and b over the `lanes` lanes of a row (a power of two; above 64 the whole workgroup), in a fixed
-// order. red: 2 floats a wave, another set for each of two calls that follow one another; every thread of the
-// workgroup calls it.
+// Sums of a and b over the `lanes` lanes of a row (a power of two), in a fixed order. red: 2 floats a wave,
+// another set for each of two calls that follow one another; every thread of the workgroup calls it.
 __device__ __forceinline__ void row_sums(float& a, float& b, int lanes, float* red) {
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
@@ -24,15 +23,15 @@ __device__ __forceinline__ void row_sums(float& a, float& b, int lanes, float* r
         }
     }
     if (lanes > 64) {
-        const int nw = blockDim.x >> 6, wave = threadIdx.x >> 6;
+        const int nw = lanes >> 6, wave = threadIdx.x >> 6, first = wave & -nw;  // the row's waves
         if ((threadIdx.x & 63) == 0) {
             red[2 * wave] = a;
             red[2 * wave + 1] = b;
         }
         __syncthreads();
-        a = red[0];
-        b = red[1];
-        for (int i = 1; i < nw; ++i) {
+        a = red[2 * first];
+        b = red[2 * first + 1];
+        for (int i = first + 1; i < first + nw; ++i) {
             a += red[2 * i];
             b += red[2 * i + 1];
         }
@@ -289,8 +288,10 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
         }
     }
     if (!a.part) return;
-    // rows that share a wave are added lane by lane; then one slot a wave (rows of up to 64 lanes) or workgroup
-    const int64_t slot = lanes > 64 ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+    // the workgroup's rows are added: those that share a wave lane by lane, then the waves through LDS in their order;
+    // a slot a workgroup
+    __shared__ Piece<DT_F32> share[kNormThreads];
+    const int wide = max(lanes, 64);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int p = at + lanes * i;
@@ -301,8 +302,19 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
                 for (int j = 0; j < 8; ++j) dw[i][j] += __shfl_xor(dw[i][j], m);
             }
         }
-        if (p < pieces && (lanes > 64 || (threadIdx.x & 63) < lanes))
-            piece_store<DT_F32>(a.part, slot * a.cols + 8 * p, piece_pack<DT_F32>(dw[i]));
+        if (wide < (int)blockDim.x) {
+            share[threadIdx.x] = piece_pack<DT_F32>(dw[i]);
+            __syncthreads();
+            for (int k = threadIdx.x + wide; k < (int)blockDim.x; k += wide) {  // (of the first rows: all others)
+                float v[8];
+                piece_values<DT_F32>(share[k], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dw[i][j] += v[j];
+            }
+            __syncthreads();
+        }
+        if (p < pieces && (int)threadIdx.x < lanes)
+            piece_store<DT_F32>(a.part, (int64_t)blockIdx.x * a.cols + 8 * p, piece_pack<DT_F32>(dw[i]));
     }
 }
 
@@ -336,11 +348,14 @@ NormGradPlan plan_rmsnorm_grad(int64_t rows, int cols, bool dw) {
     const RowPlan r = plan_row(cols, rows <= 1024);
     p.lanes = r.lanes;
     p.np = r.np;
-    p.threads = p.lanes > 64 ? p.lanes : 256;
+    // rows share a workgroup, and its part of dw, as soon as there is one for each CU (16384 rows of 1024: 29.5 us, a
+    // part for each row in flight 34.4; 2048 rows of 2048: 12.9 and 17.0)
+    p.threads = p.lanes > 64 ? p.lanes : 64;
+    while (p.threads < kNormThreads && (rows * p.lanes + p.threads - 1) / p.threads > 256) p.threads *= 2;
     const int per = p.threads / p.lanes;
-    const int64_t need = (rows + per - 1) / per, most = 256 * (512 / p.threads);
-    p.grid = (int)(need < most ? need : most);
-    p.slots = dw ? (p.lanes > 64 ? p.grid : p.grid * (p.threads / 64)) : 0;
+    const int64_t need = (rows + per - 1) / per;
+    p.grid = (int)(need < 256 ? need : 256);
+    p.slots = dw ? p.grid : 0;
     return p;
 }
 
