@@ -295,6 +295,24 @@ def test_rope_copies_the_other_channels_bit_for_bit(layer, interleaved):
         assert torch.equal(a.view(bits), y.view(bits))
 
 
+@pytest.mark.parametrize("hq,hk", [(40, 8), (37, 5), (9, 1), (255, 0)])
+def test_rope_few_tokens_are_those_of_many(layer, hq, hk):
+    """Heads are dealt to workgroups by the number of tokens: the values are the same, in place too."""
+    f, _ = layer.rotary_frequencies(96, device="cuda")
+    x = rand(gen(hq), 2100, hq + hk, 128)
+    pos = torch.arange(2100, dtype=torch.int32, device="cuda") * 61
+    for layout in (layer.HALF, layer.INTERLEAVED):
+        rotary = layer.Rotary(f, layout=layout)
+        want = layer.rope(x, rotary, pos)
+        for t0, t1 in ((0, 1), (5, 8), (100, 164), (400, 1000)):
+            y = x[t0:t1].clone()
+            part = (y[:, :hq], y[:, hq:]) if hk else y
+            got = layer.rope(part, rotary, pos[t0:t1])
+            assert torch.equal(torch.cat(got, 1) if hk else got, want[t0:t1])
+            layer.rope(part, rotary, pos[t0:t1], out=part)
+            assert torch.equal(y, want[t0:t1])
+
+
 def test_rope_batch_positions(layer, kv):
     """Positions of a cache's batch: ragged, empty sequences, rows before a sequence's first token and rows
     behind the last sequence, which keep what was there; slices of one projection, in place and not."""
