@@ -5,7 +5,8 @@
 // need no exchange and g and u never leave the chip unless they are asked for. Three kernels:
 //  - k_gated_tile: the pipelined GEMM tile (gemm_tile.h) on B slabs that hold 32 rows of Wg and the same 32
 //    of Wu in turn: 256 x 128 or 128 x 64 results a workgroup;
-//  - k_gated_stream: up to 64 rows of A, K a multiple of 128: bound by the weights' bytes;
+//  - k_gated_stream: up to 64 rows of A, or parts of so many where tiles would leave CUs idle, K a multiple of 128:
+//    bound by the weights' bytes;
 //  - k_gated_rows: what neither takes (few rows of any K, operands past 2 GiB): 32 columns a workgroup, its waves
 //    each multiply a share of K straight from memory, the shares are added through LDS in a fixed order.
 #include "device.h"

@@ -523,7 +523,7 @@ int64_t fp4_gemm_gated_workspace_bytes(const fp4_qtensor* A, const fp4_qtensor* 
  * its own. A choice of speed alone, free to change. No rows: both zero. */
 enum {
     FP4_GATED_PLAN_ROWS = 1,     /* 32 rows by 32 columns, operands straight from memory */
-    FP4_GATED_PLAN_STREAM = 2,   /* up to 64 rows, weights through LDS once */
+    FP4_GATED_PLAN_STREAM = 2,   /* few rows, or few columns: waves share K, weights through LDS once for 64 rows */
     FP4_GATED_PLAN_TILE128 = 3,  /* tiles of 128 rows by 64 columns */
     FP4_GATED_PLAN_TILE128_DEEP = 4,   /* the same, four stages deep */
     FP4_GATED_PLAN_TILE128_RAGGED = 5, /* the same for any K */
