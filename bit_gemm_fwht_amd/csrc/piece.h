@@ -159,35 +159,56 @@ __device__ __forceinline__ void piece_quantize(const QuantOut& q, float (&v)[8],
     if (valid && !(__lane_id() & 3)) q.scales[idx >> 5] = (uint8_t)(k + 127);
 }
 
-// The activation of a gated feed-forward and its derivative. 1 / (1 + e^-x) by the hardware's exponential and
-// reciprocal, an ulp each (2^-22 of the result with the argument's rounding, growing with |x| as e^-x does): the exact
-// quotient takes three times the instructions, which is what bounds the tiles' epilogue (4096 rows, K 4096, F 11008:
-// see gated.hip).
-constexpr float kSqrt2OverPi = 0.79788456080286536f, kGeluCubic = 0.044715f;
+// The activation of a gated feed-forward and its derivative, in few operations and nowhere far from fp32's own
+// rounding. Their number is what the tiles' epilogue and the coded backward pass last by: the sigmoid as
+// rcp(1 + exp(-x)) of the hardware's two instructions is off by 64 half steps (2^-24) at -80 and 17 at -20, this
+// one by 5 to -20 and 7 to -87, for 1 % of the tiles' time and of the backward pass's (4096 rows, K 4096, F 11008,
+// 4 bits: 249.4 -> 251.9 us, without g and u 227.0 -> 229.0; backward with codes 95.7 -> 96.9); with the exact quotient
+// alone a round of tiles takes 5 us more.
 
-__device__ __forceinline__ float sigmoidf(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
+// e^-y for y >= 0: 2^t by the hardware (an ulp) with t = RN(-y log2 e), times 1 + d for what t leaves of the exponent,
+// d = -y - t ln 2, which is less than 2^-17. ln 2 as one fp32 is 2^-29 off, which t passes on: a rounding at y = 20,
+// four at 87. y past 104, infinity too, is taken as 104, where the result is 0; so are results below 2^-126.
+__device__ __forceinline__ float exp_minus(float y) {
+    y = __builtin_amdgcn_fmed3f(y, 0.0f, 104.0f);  // (fminf takes two instructions)
+    const float t = -y * 1.44269504f;
+    const float d = __builtin_fmaf(t, -0.69314718f, -y);
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e, d, e);
+}
+
+// p = 1 / (1 + e^-x) and its derivative p (1 - p), both to a few roundings of themselves: with e = e^-|x| <= 1 they
+// come from 1 / (1 + e) and e / (1 + e), whose divisor lies in [1, 2] (the hardware's reciprocal: an ulp).
+__device__ __forceinline__ float sigmoid(float x, float& slope) {
+    const float e = exp_minus(fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e), s = e * r;
+    slope = r * s;
+    return x < 0.0f ? s : r;
+}
+
+// (1 + tanh z) / 2 = sigmoid(2 z): 2 z = g (2 sqrt(2 / pi) + 0.044715 * 2 sqrt(2 / pi) g^2)
+constexpr float kTanhA = 1.5957691216057308f, kTanhB = 0.07135481627260025f;
 
 __device__ __forceinline__ float act_value(float g, int act) {
-    if (act == ACT_SILU) return g * sigmoidf(g);
     if (act == ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
-    // (1 + tanh z) / 2 = sigmoid(2 z)
-    return g * sigmoidf(2.0f * kSqrt2OverPi * (g + kGeluCubic * g * g * g));
+    float unused;
+    return g * sigmoid(act == ACT_SILU ? g : g * __builtin_fmaf(g * g, kTanhB, kTanhA), unused);
 }
 
 __device__ __forceinline__ void act_slope(float g, int act, float& a, float& d) {
+    float dp;
     if (act == ACT_SILU) {
-        const float p = sigmoidf(g);
+        const float p = sigmoid(g, dp);
         a = g * p;
-        d = p * (1.0f + g * (1.0f - p));
+        d = __builtin_fmaf(g, dp, p);
     } else if (act == ACT_GELU) {
         const float p = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
         a = g * p;
         d = p + g * __expf(-0.5f * g * g) * 0.39894228040143268f;
     } else {
-        const float p = sigmoidf(2.0f * kSqrt2OverPi * (g + kGeluCubic * g * g * g));
+        const float w = g * g, p = sigmoid(g * __builtin_fmaf(w, kTanhB, kTanhA), dp);
         a = g * p;
         // (the square held finite: it meets a factor of 0 where it would not be)
-        d = p + g * p * (1.0f - p) * (2.0f * kSqrt2OverPi) * (1.0f + 3.0f * kGeluCubic * fminf(g * g, 1e37f));
+        d = __builtin_fmaf(g * dp, __builtin_fmaf(fminf(w, 1e37f), 3.0f * kTanhB, kTanhA), p);
     }
 }
 
