@@ -5,6 +5,8 @@
 // order and with the roundings of fwht_segment, so that the codes are the same as fp4_quantize's.
 #pragma once
 
+#include <type_traits>
+
 #include "device.h"
 #include "layer_internal.h"
 #include "quant_block.h"
@@ -163,8 +165,8 @@ __device__ __forceinline__ void piece_quantize(const QuantOut& q, float (&v)[8],
 // rounding. Their number is what the tiles' epilogue and the coded backward pass last by: the sigmoid as
 // rcp(1 + exp(-x)) of the hardware's two instructions is off by 64 half steps (2^-24) at -80 and 17 at -20, this
 // one by 5 to -20 and 7 to -87, for 1 % of the tiles' time and of the backward pass's (4096 rows, K 4096, F 11008,
-// 4 bits: 249.4 -> 251.9 us, without g and u 227.0 -> 229.0; backward with codes 95.7 -> 96.9); with the exact quotient
-// alone a round of tiles takes 5 us more.
+// 4 bits: 249.4 -> 251.9 us; backward with codes 95.7 -> 96.9); with the exact quotient alone a round of tiles takes
+// 5 us more.
 
 // e^-y for y >= 0: 2^t by the hardware (an ulp) with t = RN(-y log2 e), times 1 + d for what t leaves of the exponent,
 // d = -y - t ln 2, which is less than 2^-17. ln 2 as one fp32 is 2^-29 off, which t passes on: a rounding at y = 20,
@@ -185,31 +187,72 @@ __device__ __forceinline__ float sigmoid(float x, float& slope) {
     return x < 0.0f ? s : r;
 }
 
+// Phi(g) of the normal distribution, and e = e^(-g^2 / 2), both to a few roundings of themselves: (1 + erf(g / sqrt 2))
+// / 2 cancels for negative g, 4 % off at -5 and 0 at -5.8. Up to |g| = 1 it is 1 / 2 + g R(g^2), past it the tail
+// Phi(-a), a = |g|, or one minus that; the tail is e times Q(a) = erfcx(a / sqrt 2) / 2, a smooth function: s P(s) with
+// s = 1 / (1 + 0.33 a). R of degree 5 and P of degree 7 are fitted for the least relative error over [0, 1] and [1,
+// 14.6] (0.012 and 0.16 half steps). The square's own rounding, which the exponential would pass on a^2 / 2 times, goes
+// into the exponent. All of it takes less than the two branches of erff do (4096 rows, K 4096, F 11008, 4 bits: 287 ->
+// 267 us, backward with codes 117 -> 113).
+__device__ __forceinline__ float normal_cdf(float g, float& e) {
+    const float a = __builtin_amdgcn_fmed3f(fabsf(g), 0.0f, 14.5f), w = a * a;
+    const float x = exp_minus(0.5f * w);
+    e = __builtin_fmaf(-0.5f * x, __builtin_fmaf(a, a, -w), x);
+    const float s = __builtin_amdgcn_rcpf(__builtin_fmaf(a, 0.33f, 1.0f));
+    float p = __builtin_fmaf(s, 0.043525774f, -0.13791771f);
+    p = __builtin_fmaf(s, p, 0.108361416f);
+    p = __builtin_fmaf(s, p, 0.006608054f);
+    p = __builtin_fmaf(s, p, 0.10068161f);
+    p = __builtin_fmaf(s, p, 0.115317486f);
+    p = __builtin_fmaf(s, p, 0.13183379f);
+    p = __builtin_fmaf(s, p, 0.13164388f);
+    const float tail = e * (s * p);
+    float r = __builtin_fmaf(w, -7.654211e-6f, 1.1348638e-4f);
+    r = __builtin_fmaf(w, r, -1.18633e-3f);
+    r = __builtin_fmaf(w, r, 9.973323e-3f);
+    r = __builtin_fmaf(w, r, -6.649036e-2f);
+    r = __builtin_fmaf(w, r, 0.3989423f);
+    const float far = g < 0.0f ? tail : 1.0f - tail;
+    return a < 1.0f ? __builtin_fmaf(g, r, 0.5f) : far;
+}
+
 // (1 + tanh z) / 2 = sigmoid(2 z): 2 z = g (2 sqrt(2 / pi) + 0.044715 * 2 sqrt(2 / pi) g^2)
 constexpr float kTanhA = 1.5957691216057308f, kTanhB = 0.07135481627260025f;
 
-__device__ __forceinline__ float act_value(float g, int act) {
-    if (act == ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
     float unused;
-    return g * sigmoid(act == ACT_SILU ? g : g * __builtin_fmaf(g * g, kTanhB, kTanhA), unused);
+    if constexpr (ACT == ACT_SILU) return g * sigmoid(g, unused);
+    else if constexpr (ACT == ACT_GELU) return g * normal_cdf(g, unused);
+    else return g * sigmoid(g * __builtin_fmaf(g * g, kTanhB, kTanhA), unused);
 }
 
-__device__ __forceinline__ void act_slope(float g, int act, float& a, float& d) {
+template <int ACT>
+__device__ __forceinline__ void act_slope(float g, float& a, float& d) {
     float dp;
-    if (act == ACT_SILU) {
+    if constexpr (ACT == ACT_SILU) {
         const float p = sigmoid(g, dp);
         a = g * p;
         d = __builtin_fmaf(g, dp, p);
-    } else if (act == ACT_GELU) {
-        const float p = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
+    } else if constexpr (ACT == ACT_GELU) {
+        const float p = normal_cdf(g, dp);
         a = g * p;
-        d = p + g * __expf(-0.5f * g * g) * 0.39894228040143268f;
+        d = __builtin_fmaf(g * 0.39894228040143268f, dp, p);
     } else {
         const float w = g * g, p = sigmoid(g * __builtin_fmaf(w, kTanhB, kTanhA), dp);
         a = g * p;
         // (the square held finite: it meets a factor of 0 where it would not be)
         d = __builtin_fmaf(g * dp, __builtin_fmaf(fminf(w, 1e37f), 3.0f * kTanhB, kTanhA), p);
     }
+}
+
+// f(ACT) of the call's activation. Chosen once for all the values of a tile: value by value, each activation pays for
+// the registers and the code of the others (SiLU, 4096 rows: 243.9 us chosen once, 9 more value by value).
+template <typename F>
+__device__ __forceinline__ void by_act(int act, F f) {
+    if (act == ACT_SILU) f(std::integral_constant<int, ACT_SILU>{});
+    else if (act == ACT_GELU) f(std::integral_constant<int, ACT_GELU>{});
+    else f(std::integral_constant<int, ACT_GELU_TANH>{});
 }
 
 }  // namespace bgf

@@ -10,6 +10,11 @@ are off by an ulp, 2 E24 at most.
 - slopes are p + g p (1 - p) z'(g): each term's factors and products, of the sum of the terms' magnitudes: 2 * 8.5, four
   products and sums, and for tanh the argument's error in both p and 1 - p and 3 roundings in z': SLOPE = 24, + twice
   the value's share of |z|.
+- Phi(-a) = e^(-a^2/2) s P(s), a >= 1: exponential 2, its two corrections 1 each; s off by 3 (sum, reciprocal), which
+  s P(s) passes on up to 2.1 times, and the polynomial's roundings of constants and sums up to 3.4, together 9.7 at most
+  (running error of the eight steps); the fit 0.2, two products 2; with g's product 17, + 0.05 a^2 / 2. Below 1 the sum
+  1 / 2 + g R is off by 2.8 of g R, which is at most 0.34, and a rounding of itself, at least 0.16: 7, with g's product
+  8. TAIL = 17; for positive g less. Slope: Phi and g e^(-a^2/2) / sqrt(2 pi), which SLOPE covers both.
 Values below 2^-126 / (1 - p) may vanish: |g| 2^-125."""
 import math
 
@@ -20,10 +25,11 @@ import torch
 pytestmark = pytest.mark.gpu
 
 E24 = 2.0 ** -24
-VALUE, SLOPE = 10.0, 24.0
-PER_Z = {0: 0.05, 2: 4.05}  # of SILU, TANH
+VALUE, TAIL, SLOPE = 10.0, 17.0, 24.0
+PER_Z = {0: 0.05, 1: 0.05, 2: 4.05}  # of the exponent
 A, B = 2.0 * math.sqrt(2.0 / math.pi), 2.0 * math.sqrt(2.0 / math.pi) * 0.044715
 SILU, GELU, TANH = 0, 1, 2
+erfc = np.vectorize(math.erfc, otypes=[float])
 
 
 @pytest.fixture(scope="module")
@@ -45,8 +51,12 @@ def f64(t):
 
 
 def exact(g, act):
-    """Value, slope, the sum of the slope's terms' magnitudes and the argument of the sigmoid, in 64 bits without
+    """Value, slope, the sum of the slope's terms' magnitudes and the exponent, in 64 bits without
     cancellation."""
+    if act == GELU:
+        p = 0.5 * erfc(-g / math.sqrt(2.0))
+        rest = g * np.exp(-0.5 * g * g) / math.sqrt(2.0 * math.pi)
+        return g * p, p + rest, p + np.abs(rest), 0.5 * g * g
     with np.errstate(over="ignore"):
         z = g if act == SILU else g * (A + B * g * g)
         dz = 1.0 if act == SILU else A + 3.0 * B * g * g
@@ -57,7 +67,7 @@ def exact(g, act):
 
 def value_bound(g, act):
     v, _, _, z = exact(g, act)
-    return (VALUE + PER_Z[act] * np.minimum(z, 104.0)) * E24 * np.abs(v) + np.abs(g) * 2.0 ** -125
+    return ((TAIL if act == GELU else VALUE) + PER_Z[act] * np.minimum(z, 104.0)) * E24 * np.abs(v) + np.abs(g) * 2.0 ** -125
 
 
 def slope_bound(g, act):
@@ -77,7 +87,7 @@ def within(got, want, tol, what):
     assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {(err / np.maximum(tol, 1e-300)).max():.3g} of the bound"
 
 
-@pytest.mark.parametrize("act", [SILU, TANH])
+@pytest.mark.parametrize("act", [SILU, GELU, TANH])
 def test_value_and_slope(layer, act):
     """dh = u = 1: the gradients are the slope and the value themselves."""
     g = arguments()
@@ -103,7 +113,7 @@ KERNELS = [("PLAN_ROWS", 5, 96, 96), ("PLAN_STREAM", 3, 96, 512), ("PLAN_STREAM"
            ("PLAN_TILE256", 1100, 3328, 256)]
 
 
-@pytest.mark.parametrize("act", [SILU, TANH])
+@pytest.mark.parametrize("act", [SILU, GELU, TANH])
 @pytest.mark.parametrize("plan,m,f,k", KERNELS)
 def test_forward_in_every_kernel(fp4, layer, plan, m, f, k, act):
     """h against act(g) u of the g and u that the call itself kept in fp32."""
