@@ -359,17 +359,32 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
 
 class Rotary:
     """What a model keeps of its positions: inv_freq fp64 [rotary_dim / 2] on the device, the layout of the
-    pairs (HALF: channel i with i + rotary_dim / 2; INTERLEAVED: 2 i with 2 i + 1) and the rotated values' scale."""
+    pairs (HALF: channel i with i + rotary_dim / 2; INTERLEAVED: 2 i with 2 i + 1) and the rotated values' scale.
+    All three may be assigned: a call takes them as they then are."""
 
     def __init__(self, inv_freq: torch.Tensor, layout: int = HALF, scale: float = 1.0):
-        if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or not inv_freq.is_cuda or not inv_freq.is_contiguous() \
-                or inv_freq.shape[0] == 0:
-            raise ValueError("inv_freq must be a contiguous float64 CUDA vector (rotary_frequencies makes one)")
         if layout not in (HALF, INTERLEAVED):
             raise ValueError("layout must be HALF or INTERLEAVED")
-        self.inv_freq, self.layout, self.scale, self.device = inv_freq, layout, float(scale), inv_freq.device
-        self.rotary_dim = 2 * inv_freq.shape[0]
-        self._ptr, self._index = inv_freq.data_ptr(), inv_freq.get_device()
+        self.inv_freq, self.layout, self.scale = inv_freq, layout, float(scale)
+
+    @property
+    def inv_freq(self) -> torch.Tensor:
+        return self._inv_freq
+
+    @inv_freq.setter
+    def inv_freq(self, f: torch.Tensor) -> None:
+        if f.dim() != 1 or f.dtype != torch.float64 or not f.is_cuda or not f.is_contiguous() or f.shape[0] == 0:
+            raise ValueError("inv_freq must be a contiguous float64 CUDA vector (rotary_frequencies makes one)")
+        self._inv_freq, self._device, self._dim = f, f.device, 2 * f.shape[0]
+        self._ptr, self._index = f.data_ptr(), f.get_device()
+
+    @property
+    def device(self):
+        return self._device
+
+    @property
+    def rotary_dim(self) -> int:
+        return self._dim
 
 
 def rope(x, rotary: Rotary, positions, out=None, backward: bool = False):
@@ -379,7 +394,10 @@ def rope(x, rotary: Rotary, positions, out=None, backward: bool = False):
     x itself for in place. backward=True turns the other way: the gradient of x from that of the result."""
     pair = not isinstance(x, torch.Tensor)
     a, b = x if pair else (x, None)
-    index, dev = rotary._index, rotary.device
+    f = rotary._inv_freq
+    if f.data_ptr() != rotary._ptr:  # the tensor has been given other memory
+        rotary.inv_freq = f
+    index, dev = rotary._index, rotary._device
     if index != _device():
         return _there(index, rope, x, rotary, positions, out, backward)
     dtype = a.dtype
@@ -417,7 +435,7 @@ def rope(x, rotary: Rotary, positions, out=None, backward: bool = False):
         x1 = y1 = None
         x1_ld = x1_head = o1_ld = o1_head = 0
     c = RopeC(a.data_ptr(), x1, o.data_ptr(), y1, x_ld, x1_ld, x_head, x1_head, o_ld, o1_ld, o_head, o1_head, heads, heads_b, tokens,
-              rotary._ptr, pos, batch, rotary.scale, code, dim, rotary.rotary_dim, rotary.layout, backward)
+              rotary._ptr, pos, batch, rotary.scale, code, dim, rotary._dim, rotary.layout, backward)
     st = lib().fp4_rope(ctypes.addressof(c), _stream(index))
     if st:
         _check(st, "fp4_rope")
@@ -441,23 +459,61 @@ def _heads(t: torch.Tensor, tokens, dim, dtype, index: int, name: str):
 
 class GatedWeights:
     """Gate and up projection [F, K], quantized alike (MXFP4 in groups of 32 or 32 x 32 tiles, or MXFP8), with the
-    activation between them: checked once, described to the library from then on. up=None: gate is [2 F, K],
-    the gate's rows first."""
+    activation between them: checked and described to the library once, and again where one of the tensors has become
+    another (quantized anew with out=, or assigned). up=None: gate is [2 F, K], the gate's rows first."""
 
     def __init__(self, gate: QTensor, up: QTensor | None = None, act: int = SILU):
         if act not in (SILU, GELU, GELU_TANH):
             raise ValueError("act must be SILU, GELU or GELU_TANH")
-        if up is None:
-            gate, up = _halves(gate)
-        if (gate.rows, gate.cols) != (up.rows, up.cols):
-            raise ValueError(f"gate is {(gate.rows, gate.cols)}, up {(up.rows, up.cols)}")
-        self.device = gate.codes.device
-        for q, name in ((gate, "gate"), (up, "up")):
-            fp4._check_q(q, q.rows, q.cols, q.params, self.device, name)
-        self.gate, self.up, self.act, self.ff, self.hidden = gate, up, act, gate.rows, gate.cols
-        self._index = gate.codes.get_device()
-        self._c = gate.c(), up.c()
-        self._p = tuple(ctypes.addressof(c) for c in self._c)
+        self.act = act
+        self._whole, self._whole_seen = (gate, None) if up is None else (None, None)
+        self.gate, self.up = gate, up
+        self._seen = None
+        self._now()
+
+    @property
+    def device(self):
+        return self.gate.codes.device
+
+    @property
+    def ff(self) -> int:
+        return self.gate.rows
+
+    @property
+    def hidden(self) -> int:
+        return self.gate.cols
+
+    def _now(self):
+        """(addresses of both descriptions, F, K, device index, device, the descriptions) of the tensors as they are."""
+        if self._whole is not None and not _is(self._whole, self._whole_seen):
+            self.gate, self.up = _halves(self._whole)
+            self._whole_seen = _mark(self._whole)
+        g, u, seen = self.gate, self.up, self._seen
+        if seen is not None and _is(g, seen[0]) and _is(u, seen[1]):
+            return seen[2]
+        if (g.rows, g.cols) != (u.rows, u.cols):
+            raise ValueError(f"gate is {(g.rows, g.cols)}, up {(u.rows, u.cols)}")
+        dev = g.codes.device
+        for q, name in ((g, "gate"), (u, "up")):
+            fp4._check_q(q, q.rows, q.cols, q.params, dev, name)
+        c = g.c(), u.c()
+        p = ctypes.addressof(c[0]), ctypes.addressof(c[1])
+        now = p, g.rows, g.cols, g.codes.get_device(), dev, c
+        self._seen = _mark(g), _mark(u), now
+        return now
+
+
+def _mark(q: QTensor):
+    return q, q.codes, q.scales, q.params, q.rows, q.cols, q.codes.data_ptr(), q.scales.data_ptr()
+
+
+def _is(q: QTensor, mark) -> bool:
+    """Whether q is what it was when it was marked, whatever its buffers hold."""
+    if mark is None:
+        return False
+    was, codes, scales, params, rows, cols, codes_at, scales_at = mark
+    return q is was and q.codes is codes and q.scales is scales and q.params is params and q.rows == rows and q.cols == cols \
+        and codes.data_ptr() == codes_at and scales.data_ptr() == scales_at
 
 
 def _halves(q: QTensor):
@@ -483,11 +539,12 @@ def gated(a: QTensor, weights: GatedWeights, out_dtype=torch.bfloat16, out: torc
     """act(a gate^T) * (a up^T) of a [rows, K] in one pass (fp32 accumulation). keep_h=False skips h itself where
     out_q asks for its codes; keep_gu: True for a new [rows, 2 F] tensor of out_dtype with both products, or one to
     write to."""
-    dev, index, rows, ff, cols = weights.device, weights._index, a.rows, weights.ff, a.cols
+    (pg, pu), ff, hidden, index, dev, _held = weights._now()  # alive until the call has returned
+    rows, cols = a.rows, a.cols
     if index != _device():
         return _there(index, gated, a, weights, out_dtype, out, keep_h, keep_gu, out_q, q_out, workspace)
-    if cols != weights.hidden:
-        raise ValueError(f"a has {cols} columns, the weights {weights.hidden}")
+    if cols != hidden:
+        raise ValueError(f"a has {cols} columns, the weights {hidden}")
     _codes(a, rows, cols, a.params, index, "a")
     dtype = out_dtype if out is None else out.dtype
     code = _CODES.get(dtype)
@@ -509,7 +566,7 @@ def gated(a: QTensor, weights: GatedWeights, out_dtype=torch.bfloat16, out: torc
         ldgu, p = _matrix(gu, (rows, 2 * ff), dtype, index, "keep_gu"), gu.data_ptr()
     c = GatedC(h, p, ldh, ldgu, code, weights.act)
     ac = fp4.QTensorC(a.codes.data_ptr(), a.scales.data_ptr(), None, rows, cols, _params_c(a.params))
-    L, pa, po, (pg, pu) = lib(), ctypes.addressof(ac), ctypes.addressof(c), weights._p
+    L, pa, po = lib(), ctypes.addressof(ac), ctypes.addressof(c)
     qp = qa = ws = None
     need = 0
     if out_q is not None:
@@ -532,10 +589,11 @@ def gated(a: QTensor, weights: GatedWeights, out_dtype=torch.bfloat16, out: torc
 
 def gated_plan(rows: int, weights: GatedWeights, dtype=torch.bfloat16, out_q: Params | None = None) -> GatedPlanC:
     """How gated() of a [rows, K] would be carried out: kernel (PLAN_...), quantize_pass."""
+    (pg, pu), _, hidden, _, _, _held = weights._now()
     p = weights.gate.params
-    ac = fp4.QTensorC(None, None, None, rows, weights.hidden, Params(elem=p.elem, hadamard_n=p.hadamard_n).c())
+    ac = fp4.QTensorC(None, None, None, rows, hidden, Params(elem=p.elem, hadamard_n=p.hadamard_n).c())
     c, plan = GatedC(dtype=_code(dtype, "out"), act=weights.act), GatedPlanC()
-    _check(lib().fp4_gemm_gated_plan(ctypes.addressof(ac), *weights._p, ctypes.addressof(c),
+    _check(lib().fp4_gemm_gated_plan(ctypes.addressof(ac), pg, pu, ctypes.addressof(c),
                                      None if out_q is None else ctypes.addressof(_params_c(out_q)), ctypes.addressof(plan)),
            "fp4_gemm_gated_plan")
     return plan
