@@ -603,18 +603,32 @@ static hipError_t launch_stream_d(const GemmArgs& g, hipStream_t s) {
     return deep ? launch_stream<FP8, OUT, FQ, NC, MT, 2>(g, s) : launch_stream<FP8, OUT, FQ, NC, MT, 1>(g, s);
 }
 
+// Whether 48 columns a workgroup are faster than 16 for 33 to 64 rows of A in 8 bits, where A's rows are most of a unit
+// and one such workgroup fills a CU: only where their number fills the rounds that it takes, and K is long enough for
+// their bare start and end (64 rows, us of 48 and of 16 columns; 256 CUs). One round from 3/4 full: K 4096, F 9216 22.4
+// and 24.2, F 11008 29.6 and 32.6, K 8192, F 9216 52.5 and 67.7; F 12320, a second round for one workgroup, 50.2 and
+// 42.5. Several from 7/8 full: K 4096, F 21504 62.0 and 66.1, F 24576 62.9 and 69.4; F 14336, 0.58 full, 56.6 and 45.7,
+// F 28672, 0.78, 87.2 and 80.4. K from 8192 on from 3/4 full: F 28672 151.5 and 161.0; F 16384, 0.67, 99.7 and 92.7. K
+// 2048: F 12288 16.3 and 14.1, F 24576 35.6 and 31.6.
+static bool columns48(const GemmArgs& g, int cus) {
+    const int64_t groups = (g.N + 47) / 48, places = (groups + cus - 1) / cus * cus;
+    const int eighths = places == cus || g.K >= 8192 ? 6 : 7;
+    return g.M > 32 && g.M <= 64 && g.K >= 4096 && 8 * groups >= eighths * places;
+}
+
 template <bool FP8, int OUT, int FQ>
 static hipError_t launch_stream_m(const GemmArgs& g, hipStream_t s) {
     // 16 columns a workgroup, so that several fit a CU and all are resident at once; 32 where groups of 32 are
-    // quantized; 48 where A's rows are most of an 8-bit unit and F still gives most of the 256 CUs a workgroup (48
-    // rows, K 4096, F 11008: 24.6 us against 29.0; K 8192, F 4096: 30.6 against 19.3); 32, two buffers deep, where
-    // that makes no more workgroups than CUs of what would be up to twice as many, and a wave has two units (256 rows,
-    // K 4096, F 1376: 10.7 us against 11.8, 8 bits 14.8 against 18.2; 64 rows of F 5504 10.4 and 11.5, 15.2 and 18.0;
-    // K 256, 512 rows of F 1024: 5.5 against 4.4)
+    // quantized; 48 in 8 bits by columns48; 32, two buffers deep, where that makes no more workgroups than CUs of what
+    // would be up to twice as many, and a wave has two units (256 rows, K 4096, F 1376: 10.7 us against 11.8, 8 bits
+    // 14.8 against 18.2; 64 rows of F 5504 10.4 and 11.5, 15.2 and 18.0; K 256, 512 rows of F 1024: 5.5 against 4.4)
     constexpr int NC = FQ != FQ_NONE ? 2 : 1;
     const int64_t rows = (g.M + stream_parts(g.M) - 1) / stream_parts(g.M);
+    int cus = 0;
+    const hipError_t e = cu_count(&cus);
+    if (e != hipSuccess) return e;
     if constexpr (FP8 && FQ == FQ_NONE) {
-        if (g.M <= 64 && g.M > 32 && g.N >= 48 * 192)
+        if (columns48(g, cus))
             return g.M <= 48 ? launch_stream<FP8, OUT, FQ, 3, 3, 2>(g, s) : launch_stream<FP8, OUT, FQ, 3, 4, 1>(g, s);
     }
     if constexpr (FQ == FQ_NONE) {

@@ -1,0 +1,95 @@
+"""GPU tests of the variants that the calls between a layer's products choose by size, type and rounding: large calls past
+the caches, many rows, wide rows, wide blocks of columns, coded outputs of every kernel. Against 64-bit forms on the
+device, codes against fp4_quantize bit for bit. E24 = 2^-24 is half a step of fp32 relative to a value."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+E24 = 2.0 ** -24
+HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: E24}
+DTYPES = [torch.bfloat16, torch.float32]
+
+
+@pytest.fixture(scope="module")
+def fp4():
+    from bit_gemm_fwht_amd import fp4 as m
+    m.lib()
+    return m
+
+
+@pytest.fixture(scope="module")
+def layer():
+    from bit_gemm_fwht_amd import layer as m
+    m.lib()
+    return m
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rand(g, *shape, size=1.0, dtype=torch.float32):
+    return torch.randn(*shape, generator=g, device="cuda").mul_(size).to(dtype)
+
+
+def near(got, want, tol, what=""):
+    bad = ~((got.double() - want).abs() <= tol)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}"
+
+
+# ---- gated products ----
+
+def operands(fp4, g, m, f, k, elem, tile=False, size=1.5):
+    a, wg, wu = rand(g, m, k), rand(g, f, k, size=size / math.sqrt(k)), rand(g, f, k, size=1.0 / math.sqrt(k))
+    pa, pw = fp4.Params(elem=elem), fp4.Params(elem=elem, block=(32, 32) if tile else (1, 32))
+    return fp4.quantize(a, pa), fp4.quantize(wg, pw), fp4.quantize(wu, pw)
+
+
+def act64(g, act):
+    """Without cancellation in either tail."""
+    if act == 0:
+        return g * torch.sigmoid(g)
+    if act == 1:
+        return g * 0.5 * torch.special.erfc(-g * math.sqrt(0.5))
+    return g * torch.sigmoid(2.0 * math.sqrt(2.0 / math.pi) * (g + 0.044715 * g ** 3))
+
+
+def act_bound(g, act):
+    """Half steps of the activation and of its product with u: 17 at most for the first two (5 of them |g|^2's share of
+    the exponent's at 13), 11 and 4 of tanh's argument for the third; values below |g| 2^-125 may vanish."""
+    v = act64(g, act).abs()
+    return ((4.1 * 2.0 * math.sqrt(2.0 / math.pi) * (g + 0.044715 * g ** 3).abs().clamp(max=104.0) if act == 2 else 0.0) + 23.0) * E24 * v \
+        + g.abs() * 2.0 ** -125
+
+
+def check_products(fp4, aq, gq, uq, act, got, dtype):
+    """g and u against the products of what the codes stand for; h against the activation of the g and u that were kept
+    (in fp32: exactly those of the accumulators; bf16: half a step of each more, the activation's slope at most 1.13)."""
+    f = gq.rows
+    a, wg, wu = (fp4.dequantize(q).double() for q in (aq, gq, uq))
+    # sums of fp32 products; blocks of 8 products lose up to 8 * 2^-13 of their largest on the FP8 matrix core
+    part = 1e-5 + (2.0 ** -10 if aq.params.elem == fp4.E4M3 else 0.0)
+    half = HALF_STEP[dtype]
+    for y, b, name in ((got.gu[:, :f], wg, "g"), (got.gu[:, f:], wu, "u")):
+        want, tol = a @ b.T, part * (a.abs() @ b.abs().T)
+        near(y, want, tol + half * (want.abs() + tol), name)
+    g, u = got.gu[:, :f].double(), got.gu[:, f:].double()
+    h = act64(g, act) * u
+    tol = act_bound(g, act) * u.abs() + half * h.abs()
+    if dtype is torch.bfloat16:
+        tol = 1.01 * (tol + half * (1.13 * g.abs() * u.abs() + h.abs()))
+    near(got.h, h, tol, "h")
+
+
+@pytest.mark.parametrize("m,f", [(33, 9216), (48, 11000), (60, 9300), (64, 12288), (40, 12320), (64, 21504)])
+def test_gated_wide_blocks_of_columns(fp4, layer, m, f):
+    """33 to 64 rows in 8 bits and long K: blocks of 48 columns where they fill the rounds that they take, others beside
+    them."""
+    aq, gq, uq = operands(fp4, gen(m), m, f, 4096, fp4.E4M3)
+    for act, dtype in ((0, torch.float32), (1, torch.bfloat16)):
+        w = layer.GatedWeights(gq, uq, act=act)
+        assert layer.gated_plan(m, w, dtype).kernel == layer.PLAN_STREAM
+        check_products(fp4, aq, gq, uq, act, layer.gated(aq, w, out_dtype=dtype, keep_gu=True), dtype)
