@@ -592,13 +592,13 @@ static hipError_t launch_stream(const GemmArgs& g, hipStream_t s) {
 }
 
 template <bool FP8, int OUT, int FQ, int NC, int MT>
-static hipError_t launch_stream_d(const GemmArgs& g, hipStream_t s) {
+static hipError_t launch_stream_d(const GemmArgs& g, int cus, hipStream_t s) {
     // two buffers where a wave has eight units or more to go through (one row, 8 bits, K 4096: 23.3 us against 24.5;
     // 4 bits, K 8192: 18.7 against 19.3), else one, which leaves room for more workgroups (4 bits, K 4096: 9.9
     // against 10.2). With more than 32 rows two buffers leave room for one workgroup a CU alone: only where there are
     // no more than that (48 rows, 4 bits, K 8192, F 11008: 31.0 us with one, 33.6 with two), and then for any K (128
     // rows, K 4096, F 1376: 7.6 against 8.7)
-    const bool alone = stream_parts(g.M) * ((g.N + 16 * NC - 1) / (16 * NC)) <= 256;
+    const bool alone = stream_parts(g.M) * ((g.N + 16 * NC - 1) / (16 * NC)) <= cus;
     const bool deep = alone || (MT <= 2 && (FP8 ? g.K / 128 : g.K / 256) >= 8 * kStreamWaves);
     return deep ? launch_stream<FP8, OUT, FQ, NC, MT, 2>(g, s) : launch_stream<FP8, OUT, FQ, NC, MT, 1>(g, s);
 }
@@ -633,13 +633,13 @@ static hipError_t launch_stream_m(const GemmArgs& g, hipStream_t s) {
     }
     if constexpr (FQ == FQ_NONE) {
         const int64_t groups = stream_groups(g.M, g.N);
-        if (rows > 32 && groups > 256 && groups <= 512 && (FP8 ? g.K / 128 : g.K / 256) >= 2 * kStreamWaves)
-            return rows <= 48 ? launch_stream_d<FP8, OUT, FQ, 2, 3>(g, s) : launch_stream_d<FP8, OUT, FQ, 2, 4>(g, s);
+        if (rows > 32 && groups > cus && groups <= 2 * cus && (FP8 ? g.K / 128 : g.K / 256) >= 2 * kStreamWaves)
+            return rows <= 48 ? launch_stream_d<FP8, OUT, FQ, 2, 3>(g, cus, s) : launch_stream_d<FP8, OUT, FQ, 2, 4>(g, cus, s);
     }
-    if (rows <= 16) return launch_stream_d<FP8, OUT, FQ, NC, 1>(g, s);
-    if (rows <= 32) return launch_stream_d<FP8, OUT, FQ, NC, 2>(g, s);
-    if (rows <= 48) return launch_stream_d<FP8, OUT, FQ, NC, 3>(g, s);
-    return launch_stream_d<FP8, OUT, FQ, NC, 4>(g, s);
+    if (rows <= 16) return launch_stream_d<FP8, OUT, FQ, NC, 1>(g, cus, s);
+    if (rows <= 32) return launch_stream_d<FP8, OUT, FQ, NC, 2>(g, cus, s);
+    if (rows <= 48) return launch_stream_d<FP8, OUT, FQ, NC, 3>(g, cus, s);
+    return launch_stream_d<FP8, OUT, FQ, NC, 4>(g, cus, s);
 }
 
 template <bool FP8, bool B2D, int OUT, int FQ, int TS, int NS, bool RAG = false>

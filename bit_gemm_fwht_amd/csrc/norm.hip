@@ -341,8 +341,11 @@ __global__ __launch_bounds__(1024) void k_sum_slots(const float* part, int slots
     }
 }
 
-// 512 threads a CU (of 256): each carries its part of dw through many rows, so that the parts, which are written and
-// read again, stay few (8192 rows of 4096: 52.7 us; with 1024 threads a CU 59.2, with 1 piece a lane 60.9).
+// 512 threads a CU: each carries its part of dw through many rows, so that the parts, which are written and
+// read again, stay few (8192 rows of 4096: 52.7 us; with 1024 threads a CU 59.2, with 1 piece a lane 60.9). The
+// number of CUs is the whole card's here and not asked of the device: it decides in which parts dw is added, and so the
+// last bits, and the size of the workspace, which a program may ask for without a device.
+constexpr int kGradGroups = 256;
 NormGradPlan plan_rmsnorm_grad(int64_t rows, int cols, bool dw) {
     NormGradPlan p;
     const RowPlan r = plan_row(cols, rows <= 1024);
@@ -351,10 +354,10 @@ NormGradPlan plan_rmsnorm_grad(int64_t rows, int cols, bool dw) {
     // rows share a workgroup, and its part of dw, as soon as there is one for each CU (16384 rows of 1024: 29.5 us, a
     // part for each row in flight 34.4; 2048 rows of 2048: 12.9 and 17.0)
     p.threads = p.lanes > 64 ? p.lanes : 64;
-    while (p.threads < kNormThreads && (rows * p.lanes + p.threads - 1) / p.threads > 256) p.threads *= 2;
+    while (p.threads < kNormThreads && (rows * p.lanes + p.threads - 1) / p.threads > kGradGroups) p.threads *= 2;
     const int per = p.threads / p.lanes;
     const int64_t need = (rows + per - 1) / per;
-    p.grid = (int)(need < 256 ? need : 256);
+    p.grid = (int)(need < kGradGroups ? need : kGradGroups);
     p.slots = dw ? p.grid : 0;
     return p;
 }
