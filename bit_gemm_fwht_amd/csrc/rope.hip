@@ -12,10 +12,11 @@ namespace bgf {
 
 constexpr int kRopeThreads = 256, kRopePairs = 512, kRopeTokens = 64, kRopeGroups = 512;
 
-// cos and sin of an angle in radians
+// cos and sin of an angle in radians, |t| < 2^45. pi / 2 as one fp64 is 6e-17 off, which n quarter turns add up: 8e-8
+// at position 2^31 for a frequency of 1, past 2^-22 for one above 3 (a table may hold any), so its rest comes along.
 __device__ __forceinline__ float2 cos_sin(double t) {
     const double n = rint(t * 0.63661977236758134);  // quarter turns: 2 / pi
-    const float r = (float)fma(-n, 1.5707963267948966, t), z = r * r;
+    const float r = (float)fma(-n, 6.123233995736766e-17, fma(-n, 1.5707963267948966, t)), z = r * r;
     // sin r = r - r^3/3! + .. - r^11/11!, cos r = 1 - r^2/2! + .. - r^10/10!: the next terms are below 2^-32
     float s = __builtin_fmaf(z, -2.50521083854e-8f, 2.75573192240e-6f);
     s = __builtin_fmaf(z, s, -1.98412698413e-4f);

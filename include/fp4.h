@@ -470,7 +470,7 @@ int fp4_rmsnorm_backward(const fp4_norm_grad* n, void* workspace, int64_t ws_byt
  *   (y1, y2) = scale * (x1 cos t - x2 sin t, x2 cos t + x1 sin t),  t = position * inv_freq[i]
  * and the others are copied. backward != 0 turns by -t: the gradient of x from that of y. inv_freq: device
  * fp64 [rotary_dim / 2], so that any scaling for long contexts is a table made once; the angle and its
- * reduction are fp64, sine and cosine fp32 (2^-22 off at most).
+ * reduction are fp64, sine and cosine fp32 (2^-22 off at most, for angles below 2^45).
  * Positions: int32 [tokens] (positions), or those of a cache's batch (batch: of the batch's fields cu_tokens,
  * context, seqs and tokens are used): row i of a sequence with n rows sits at context - n + i. Rows with no
  * token (before a sequence's first, behind the last sequence) are left as they are. Exactly one of the two

@@ -40,6 +40,34 @@ def near(got, want, tol, what=""):
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}"
 
 
+# ---- rotary positions ----
+
+def rope64(x, pos, f, interleaved, backward=False):
+    """The rotation by the fp64 products of position and frequency, and the magnitude |x1| + |x2| of each place."""
+    n = f.numel()
+    t = pos.double()[:, None, None] * f
+    c, s = t.cos(), -t.sin() if backward else t.sin()
+    x = x.double()
+    a, b = (x[..., 0:2 * n:2], x[..., 1:2 * n:2]) if interleaved else (x[..., :n], x[..., n:2 * n])
+    y = (a * c - b * s, b * c + a * s)
+    size = a.abs() + b.abs()
+    join = (lambda u, v: torch.stack([u, v], -1).flatten(-2)) if interleaved else (lambda u, v: torch.cat([u, v], -1))
+    return torch.cat([join(*y), x[..., 2 * n:]], -1), torch.cat([join(size, size), torch.zeros_like(x[..., 2 * n:])], -1)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_of_frequencies_above_one(layer, interleaved):
+    """Angles of many turns: positions to 2^31 - 1, frequencies from 2^-20 to 2^13. Sine and cosine 2^-22, two products
+    and a sum."""
+    f = torch.logspace(-20, 13, 32, base=2.0, dtype=torch.float64) * math.sqrt(0.9)
+    pos = torch.tensor([0, 1, 3, 1000, 131071, 10 ** 8, 2 ** 30 + 7, 2 ** 31 - 1, -5, -2 ** 31], dtype=torch.int32)
+    x = rand(gen(1), 10, 3, 64)
+    rotary = layer.Rotary(f.cuda(), layout=layer.INTERLEAVED if interleaved else layer.HALF)
+    for backward in (False, True):
+        want, size = rope64(x.cpu(), pos, f, interleaved, backward)
+        near(layer.rope(x, rotary, pos.cuda(), backward=backward).cpu(), want, size * (2.0 ** -22 + 3 * E24), "rope")
+
+
 # ---- gated products ----
 
 def operands(fp4, g, m, f, k, elem, tile=False, size=1.5):
