@@ -14,6 +14,7 @@ namespace {
 using namespace bgf;
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxPlaces = int64_t(1) << 58;  // of h: bytes of gu and of the workspace stay in 64 bits
 constexpr int kMaxCols = 32768;  // of a norm: a row's pieces stay in registers
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -108,6 +109,7 @@ int check_gated(const fp4_qtensor* A, const fp4_qtensor* G, const fp4_qtensor* U
     if (*kind == 1 && *b2d) return FP4_ERR_UNSUPPORTED;
     if (*b2d && F % 32) return FP4_ERR_INVALID_ARG;
     if (M > kMaxRows || F > kMaxRows || K > kMaxRows) return FP4_ERR_UNSUPPORTED;
+    if (M > 0 && F > kMaxPlaces / M) return FP4_ERR_UNSUPPORTED;
     if (out_q) {
         fp4_qtensor none{};
         QuantOut unused;

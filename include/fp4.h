@@ -501,7 +501,7 @@ int fp4_rope(const fp4_rope_args* a, void* stream);
  * in one pass over the operands. Operand pairs as for fp4_gemm without NVFP4: MXFP4 (the weights may use
  * (32, 32) tiles) or MXFP8; gate and up share one set of parameters, and A's rotation. h [M, F] and gu
  * [M, 2 F] (g, then u: what fp4_gated_backward reads) of dtype, either may be NULL; out_q / h_q as above with
- * hadamard_n <= 128 and F % 32 == 0; at least one of the three outputs. Codes 16-byte aligned, scales 4-byte
+ * hadamard_n <= 128 and F % 32 == 0; at least one of the three outputs. M, F, K below 2^31, M F up to 2^58. Codes 16-byte aligned, scales 4-byte
  * where K % 128 == 0. Pitches need not be multiples of 16 bytes (that only narrows the stores).
  * act: x / (1 + e^-x); x Phi(x) with the error function; the same with
  * Phi(x) ~ (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2.
