@@ -2,7 +2,9 @@
 //
 // Forward, a row s = RN(x + r): y = s w / sqrt(mean s^2 + eps). One pass over memory: a row's pieces of 8
 // elements (piece.h) stay in registers between the sum of squares and the output, so x and r are read once
-// and s, y and the codes written once.
+// and s, y and the codes written once. Rows past 12288 columns nearly fill them: what would spill is worked out or read
+// again (LEAN, again, apart below), and no instance uses scratch memory but one of the backward pass (bf16, 6 pieces a
+// lane: 3 registers).
 #include "device.h"
 #include "launch.h"
 #include "layer_internal.h"
@@ -61,25 +63,42 @@ __device__ __forceinline__ void weight_values(const Piece<DT_F32>& t, int kind, 
     }
 }
 
+// The lane's place as if anew: what follows from it is worked out again, not held in registers.
+__device__ __forceinline__ void again(int& at) { asm volatile("" : "+v"(at)); }
+
+// Before a piece of a row that fills the registers: its loads are not moved up to those of the pieces before, and
+// its places are worked out again, not held.
+__device__ __forceinline__ void apart(int& at) { asm volatile("" : "+v"(at)::"memory"); }
+
 // Loads are unconditional: lanes past the row's end or the last row read the last piece or row again, whose
 // values count for nothing (a load behind a condition waits for the ones before it).
 template <int IN, int NP, int FQ, bool RES, bool NT>
 __global__ __launch_bounds__(kNormThreads) void k_rmsnorm(NormArgs a, int lanes) {
     __shared__ float red[2][2 * kNormThreads / 64];
-    const int per = blockDim.x / lanes, sub = threadIdx.x / lanes, at = threadIdx.x - sub * lanes;
+    const int per = blockDim.x / lanes, sub = threadIdx.x / lanes;
+    int at = threadIdx.x - sub * lanes;
     const int pieces = a.cols >> 3;
     const float inv_cols = 1.0f / (float)a.cols;
     Piece<IN> x[NP], r[NP];
-    auto load = [&](int64_t r0) {
+    auto load = [&](int64_t r0, int i0, int i1) {
         const int64_t row = min(r0 + sub, a.rows - 1);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
+        for (int i = i0; i < i1; ++i) {
             const int p = min(at + lanes * i, pieces - 1);
             piece_load<IN, NT>(x[i], a.x, row * a.ldx + 8 * p);
             if constexpr (RES) piece_load<IN, NT>(r[i], a.r, row * a.ldr + 8 * p);
         }
     };
-    load((int64_t)blockIdx.x * per);
+    constexpr int W = 4 * Piece<IN>::N;  // registers of a piece as it is stored
+    // Where a row's fp32 values, its weight and the next row nearly fill the registers, the addresses of its pieces,
+    // which the compiler would hold from row to row, are worked out again for each (6000 rows with residual and codes,
+    // held and worked out again: 20480 columns in bf16 330 and 275 us, in fp32 459 and 359). Without a residual to carry
+    // that costs 2 to 3 % where nothing spills.
+    constexpr bool LEAN = RES ? NP >= 6 : NP * (16 + W) + (FQ != 0) > 160;
+    // The next row is loaded during the present one, but for fp32 of 8 pieces with a residual, where it has no room
+    // (6000 rows of 32768: 671 us, spilled 1037).
+    constexpr bool AHEAD = NP * (16 + W * (RES ? 2 : 1)) <= 192;
+    if constexpr (AHEAD) load((int64_t)blockIdx.x * per, 0, NP);
     // the weight stays in registers where there is room beside the next row, else it is read again for each row
     constexpr bool KEPT = NP <= 2;
     Piece<DT_F32> w[NP];
@@ -92,10 +111,17 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm(NormArgs a, int lanes)
     for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.rows; r0 += (int64_t)gridDim.x * per, turn ^= 1) {
         const int64_t row = r0 + sub;
         const bool in = row < a.rows;
+        if constexpr (LEAN) again(at);
         float v[NP][8], ss = 0.0f, none = 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int p = at + lanes * i;
+            if constexpr (!AHEAD) {
+                if (i % 2 == 0) {
+                    apart(at);
+                    load(r0, i, i + 2);
+                }
+            }
             piece_values<IN>(x[i], v[i]);
             if constexpr (RES) {
                 float rv[8];
@@ -114,12 +140,14 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm(NormArgs a, int lanes)
             for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[i][j], v[i][j], ss);
         }
         // the weight first: loads return in order; then the next row, on its way during this one's sums and codes
+        if constexpr (LEAN) again(at);
         if constexpr (!KEPT) load_weight();
-        load(r0 + (int64_t)gridDim.x * per);
+        if constexpr (AHEAD) load(r0 + (int64_t)gridDim.x * per, 0, NP);
         row_sums(ss, none, lanes, red[turn]);
         const float rstd = 1.0f / sqrtf(ss * inv_cols + a.eps);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
+            if constexpr (LEAN) again(at);
             const int p = at + lanes * i;
             const bool here = in && p < pieces;
             float wv[8];
@@ -208,11 +236,21 @@ hipError_t launch_rmsnorm(const NormArgs& a, int dtype, int rnd, hipStream_t s) 
 template <int IN, int NP, bool NT>
 __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, int lanes) {
     __shared__ float red[2][2 * kNormThreads / 64];
-    const int per = blockDim.x / lanes, sub = threadIdx.x / lanes, at = threadIdx.x - sub * lanes;
+    const int per = blockDim.x / lanes, sub = threadIdx.x / lanes;
+    int at = threadIdx.x - sub * lanes;
     const int pieces = a.cols >> 3;
     const float inv_cols = 1.0f / (float)a.cols;
+    // What a lane holds of a row from the sums to the result: all three inputs and the weight where they fit beside its
+    // part of dw, else s and dy, or s alone; the others are read again where they are used (6000 rows, spilled and read
+    // again: 32768 columns in bf16 578 and 424 us, in fp32 1272 and 712; 24576 in fp32 586 and 497).
+    constexpr int W = 4 * Piece<IN>::N;
+    constexpr bool ALL = NP * (16 + 3 * W) <= 168, DS = NP * (8 + 3 * W) <= 128, DY = NP * (8 + 2 * W) <= 160;
+    constexpr int NW = ALL ? NP : 1, NS = DS ? NP : 1, ND = DY ? NP : 1;
     struct Row {
-        Piece<IN> s[NP], dy[NP], ds[NP];
+        Piece<IN> s[NP], dy[ND], ds[NS];
+    };
+    auto load_dy = [&](Piece<IN>& t, int64_t r0, int i) {
+        piece_load<IN, NT>(t, a.dy, min(r0 + sub, a.rows - 1) * a.lddy + 8 * min(at + lanes * i, pieces - 1));
     };
     auto load = [&](Row& t, int64_t r0) {  // without conditions, as in the forward pass
         const int64_t row = min(r0 + sub, a.rows - 1);
@@ -220,9 +258,11 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
         for (int i = 0; i < NP; ++i) {
             const int p = min(at + lanes * i, pieces - 1);
             piece_load<IN, NT>(t.s[i], a.s, row * a.lds + 8 * p);
-            piece_load<IN, NT>(t.dy[i], a.dy, row * a.lddy + 8 * p);
-            if (a.dsum) piece_load<IN, NT>(t.ds[i], a.dsum, row * a.lddsum + 8 * p);
-            else piece_zero<IN>(t.ds[i]);
+            if constexpr (DY) load_dy(t.dy[i], r0, i);
+            if constexpr (DS) {
+                if (a.dsum) piece_load<IN, NT>(t.ds[i], a.dsum, row * a.lddsum + 8 * p);
+                else piece_zero<IN>(t.ds[i]);
+            }
         }
     };
     // the next row is loaded during the present one where both fit the registers
@@ -231,17 +271,22 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
     Row next;
     if constexpr (AHEAD) load(next, (int64_t)blockIdx.x * per);
     float dw[NP][8];
-    Piece<DT_F32> w[NP];
+    Piece<DT_F32> w[NW];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        weight_load(w[i], a.w, a.w_kind, min(at + lanes * i, pieces - 1));
+        if constexpr (ALL) weight_load(w[i], a.w, a.w_kind, min(at + lanes * i, pieces - 1));
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
     }
+    auto weight = [&](int i, float (&v)[8]) {
+        if constexpr (!ALL) weight_load(w[0], a.w, a.w_kind, min(at + lanes * i, pieces - 1));
+        weight_values(w[ALL ? i : 0], a.w_kind, v);
+    };
     int turn = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.rows; r0 += step, turn ^= 1) {
         const int64_t row = r0 + sub;
         const bool in = row < a.rows;
+        if constexpr (NP >= 4) again(at);
         Row t;
         if constexpr (AHEAD) {
             t = next;
@@ -252,11 +297,14 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
         float ss = 0.0f, as = 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
+            if constexpr (!ALL) apart(at);
+            else if constexpr (NP >= 6) again(at);
             const bool here = in && at + lanes * i < pieces;
             float sv[8], dv[8], wv[8];
             piece_values<IN>(t.s[i], sv);
-            piece_values<IN>(t.dy[i], dv);
-            weight_values(w[i], a.w_kind, wv);
+            if constexpr (!DY) load_dy(t.dy[0], r0, i);
+            piece_values<IN>(t.dy[DY ? i : 0], dv);
+            weight(i, wv);
             float q = 0.0f, d = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -265,19 +313,34 @@ __global__ __launch_bounds__(kNormThreads) void k_rmsnorm_grad(NormGradArgs a, i
             }
             ss += here ? q : 0.0f;
             as += here ? d : 0.0f;
+            if constexpr (!ALL) asm volatile("" : "+v"(ss), "+v"(as));  // (added now: the piece's values are done with)
         }
+        if constexpr (NP >= 4) again(at);
         row_sums(ss, as, lanes, red[turn]);
         const float rstd = 1.0f / sqrtf(ss * inv_cols + a.eps);
         const float c = as * inv_cols * rstd * rstd;  // mean(a n) r: dx = r (a - s c) + dsum
+        if constexpr (NP >= 6) {  // as they were loaded: else their values and products are held from the sums to here
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+#pragma unroll
+                for (int k = 0; k < Piece<IN>::N; ++k) asm volatile("" : "+v"(t.s[i].w[k]), "+v"(t.dy[DY ? i : 0].w[k]));
+        }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
+            if constexpr (!ALL) apart(at);
+            else if constexpr (NP >= 6) again(at);
             const int p = at + lanes * i;
             const bool here = in && p < pieces;
             float sv[8], dv[8], wv[8], o[8], base[8];
             piece_values<IN>(t.s[i], sv);
-            piece_values<IN>(t.dy[i], dv);
-            piece_values<IN>(t.ds[i], base);
-            weight_values(w[i], a.w_kind, wv);
+            if constexpr (!DY) load_dy(t.dy[0], r0, i);
+            piece_values<IN>(t.dy[DY ? i : 0], dv);
+            if constexpr (!DS) {
+                if (a.dsum) piece_load<IN, NT>(t.ds[0], a.dsum, min(row, a.rows - 1) * a.lddsum + 8 * min(p, pieces - 1));
+                else piece_zero<IN>(t.ds[0]);
+            }
+            piece_values<IN>(t.ds[DS ? i : 0], base);
+            weight(i, wv);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 o[j] = __builtin_fmaf(rstd, dv[j] * wv[j] - sv[j] * c, base[j]);

@@ -40,6 +40,39 @@ def near(got, want, tol, what=""):
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}"
 
 
+# ---- norm ----
+
+# A row's sum runs through at most 8 * 8 additions in a lane, 6 across a wave and 8 across waves.
+DEPTH = 80
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(5, 20480), (300, 24576), (1200, 14336), (1100, 20480), (700, 32768), (2, 26000), (6200, 4096)])
+def test_norm_backward_of_wide_rows(layer, rows, cols, dtype):
+    """Rows that nearly fill the registers, and a call past the caches; in place of both gradients too."""
+    g = gen(rows * 3 + cols)
+    s, dy, ds = (rand(g, rows, cols, size=z, dtype=dtype) for z in (2.0, 0.3, 0.5))
+    w = rand(g, cols, dtype=torch.bfloat16 if rows & 1 else torch.float32)
+    dx, dw = layer.rmsnorm_backward(dy, s, w, eps=0.25, dsum=ds)
+    s64, dy64, ds64 = s.double(), dy.double(), ds.double()
+    r = torch.rsqrt(s64.square().mean(1, keepdim=True) + 0.25)
+    n, a = s64 * r, dy64 * w.double()
+    want = ds64 + r * (a - n * (a * n).mean(1, keepdim=True))
+    # both sums DEPTH roundings of their magnitudes, the root another half; a few for the rest
+    tol = (2 * DEPTH + 16) * E24 * (ds64.abs() + r * (a.abs() + n.abs() * (a * n).abs().mean(1, keepdim=True)))
+    near(dx, want, tol + HALF_STEP[dtype] * want.abs(), "dx")
+    # a column's terms: n (half the sum's depth and 5), a product; the rows of a workgroup one after another, 3 steps
+    # across a wave's rows, 7 across its waves, then at most 256 parts in 128 runs of 2, two steps and 32 runs
+    depth = DEPTH / 2 + 6 + math.ceil(rows / 256) + 3 + 7 + 2 + 2 + 32
+    near(dw, (dy64 * n).sum(0), depth * E24 * (dy64 * n).abs().sum(0), "dw")
+    for out in (0, 1):
+        t = dy.clone(), ds.clone()
+        x2, w2 = layer.rmsnorm_backward(t[0], s, w, eps=0.25, dsum=t[1], out=t[out])
+        assert torch.equal(x2, dx) and torch.equal(w2, dw)
+    x2, _ = layer.rmsnorm_backward(dy, s, w, eps=0.25, dweight=False)
+    near(x2, want - ds64, tol + HALF_STEP[dtype] * (want - ds64).abs(), "dx without a stream")
+
+
 # ---- rotary positions ----
 
 def rope64(x, pos, f, interleaved, backward=False):
