@@ -40,10 +40,78 @@ def near(got, want, tol, what=""):
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}"
 
 
+def params(fp4, elem, hn, ceil, sr, seed=5):
+    return fp4.Params(elem=elem, hadamard_n=hn, scale_mode=fp4.SCALE_E8M0_CEIL if ceil else fp4.SCALE_E8M0_FLOOR,
+                      round_mode=fp4.ROUND_SR if sr else fp4.ROUND_RNE, seed=seed)
+
+
+def same_codes(q, want):
+    assert (q.rows, q.cols, q.params) == (want.rows, want.cols, want.params)
+    assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
+
+
 # ---- norm ----
 
 # A row's sum runs through at most 8 * 8 additions in a lane, 6 across a wave and 8 across waves.
 DEPTH = 80
+# More rows than 4 a CU (workgroups that go through several, the last ones not all there), one to eight pieces a lane,
+# rows that share a wave and rows that span eight; 6200 x 4096 reads past the caches.
+MANY = [(2500, 64), (5003, 256), (9001, 1000), (1300, 4096), (1100, 5120), (1025, 9000), (1200, 14336), (1100, 20480),
+        (1030, 32768), (6200, 4096)]
+
+
+def norm64(s, w, eps):
+    s = s.double()
+    return s * torch.rsqrt(s.square().mean(1, keepdim=True) + eps) * w.double()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", MANY)
+def test_norm_of_many_rows(layer, rows, cols, dtype):
+    g = gen(rows + cols)
+    x, r = rand(g, rows, cols, dtype=dtype), rand(g, rows, cols, size=3.0, dtype=dtype)
+    w = rand(g, cols, dtype=torch.bfloat16 if rows & 1 else torch.float32)
+    for res in (None, r):
+        got = layer.rmsnorm(x, w, eps=0.125, residual=res)
+        s = x if res is None else (x.float() + res.float()).to(dtype)
+        assert res is None or torch.equal(got.sum, s)
+        want = norm64(s, w, 0.125)
+        # 1 / sqrt: half the sum's error; the mean, eps, root, quotient and two products round once each
+        near(got.y, want, want.abs() * ((DEPTH / 2 + 6) * E24 + HALF_STEP[dtype]), "y")
+    a, b = x.clone(), r.clone()
+    inside = layer.rmsnorm(a, w, eps=0.125, residual=b, sum_out=a, out=torch.empty_like(x))
+    assert inside.sum is a and torch.equal(a, got.sum) and torch.equal(inside.y, got.y) and torch.equal(b, r)
+    layer.rmsnorm(a.copy_(x), w, eps=0.125, residual=b, sum_out=b)
+    assert torch.equal(b, got.sum)
+    y = layer.rmsnorm(x, w, eps=0.125).y
+    layer.rmsnorm(a.copy_(x), w, eps=0.125, out=a)
+    assert torch.equal(a, y)
+
+
+@pytest.mark.parametrize("elem,hn,ceil,sr", [(1, 128, 1, 0), (0, 32, 0, 0), (0, 128, 1, 1), (1, 0, 0, 1)])
+@pytest.mark.parametrize("rows,cols", [(2500, 128), (5003, 256), (1300, 4096), (1100, 5120), (1200, 14336), (1100, 20480),
+                                       (1030, 32768), (6200, 4096)])
+def test_norm_codes_of_many_rows(fp4, layer, rows, cols, elem, hn, ceil, sr):
+    g = gen(rows + cols)
+    x, r, w = rand(g, rows, cols, dtype=torch.bfloat16), rand(g, rows, cols, dtype=torch.bfloat16), rand(g, cols)
+    p = params(fp4, elem, hn, ceil, sr)
+    full = layer.rmsnorm(x.float(), w, out_q=p)  # the output before it is rounded: fp32 in, fp32 out
+    same_codes(full.q, fp4.quantize(full.y, p))
+    got = layer.rmsnorm(x, w, out_q=p)
+    same_codes(got.q, full.q)
+    assert torch.equal(got.y, full.y.bfloat16())
+    res = layer.rmsnorm(x, w, residual=r, out_q=p, keep_y=False)
+    assert res.y is None and torch.equal(res.sum, (x.float() + r.float()).bfloat16())
+    full = layer.rmsnorm(res.sum.float(), w, out_q=p)
+    same_codes(res.q, full.q)
+    layer.rmsnorm(x, w, residual=r, sum_out=x, out_q=p, keep_y=False, q_out=got.q)
+    assert torch.equal(x, res.sum)
+    same_codes(got.q, full.q)
+    # in fp32 with a residual: its own instances
+    x32, r32 = x.float(), r.float()
+    res = layer.rmsnorm(x32, w, residual=r32, out_q=p)
+    same_codes(res.q, fp4.quantize(res.y, p))
+    assert torch.equal(res.sum, x32 + r32)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
