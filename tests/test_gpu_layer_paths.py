@@ -222,3 +222,130 @@ def test_gated_wide_blocks_of_columns(fp4, layer, m, f):
         w = layer.GatedWeights(gq, uq, act=act)
         assert layer.gated_plan(m, w, dtype).kernel == layer.PLAN_STREAM
         check_products(fp4, aq, gq, uq, act, layer.gated(aq, w, out_dtype=dtype, keep_gu=True), dtype)
+
+
+def plan_name(layer, plan):
+    return next(n for n in dir(layer) if n.startswith("PLAN_") and getattr(layer, n) == plan)
+
+
+# every kernel, by its plan: few rows of any K, streams, the three kinds of 128-row tiles, 256-row tiles
+CODED = [("PLAN_ROWS", 1, 128, 96), ("PLAN_ROWS", 20, 160, 160), ("PLAN_ROWS", 32, 128, 1120), ("PLAN_STREAM", 3, 128, 384),
+         ("PLAN_STREAM", 60, 256, 1024), ("PLAN_STREAM", 130, 1408, 512), ("PLAN_TILE128", 200, 11008, 256), ("PLAN_TILE128_DEEP", 90, 6016, 384),
+         ("PLAN_TILE128_RAGGED", 33, 128, 96), ("PLAN_TILE128_RAGGED", 150, 640, 288), ("PLAN_TILE256", 1030, 3328, 384)]
+
+
+@pytest.mark.parametrize("act", [0, 1, 2])
+@pytest.mark.parametrize("kind", ["e2m1", "tile", "e4m3"])
+@pytest.mark.parametrize("plan,m,f,k", CODED)
+def test_gated_codes_of_every_kernel(fp4, layer, plan, m, f, k, kind, act):
+    """Weights in groups and in 32 x 32 tiles, the three activations: codes of the fp32 output as fp4_quantize makes them,
+    whatever else is stored."""
+    aq, gq, uq = operands(fp4, gen(m + f), m, f, k, fp4.E4M3 if kind == "e4m3" else fp4.E2M1, kind == "tile")
+    w = layer.GatedWeights(gq, uq, act=act)
+    assert plan_name(layer, layer.gated_plan(m, w).kernel) == plan
+    for elem, hn, ceil, sr in ((0, 0, 0, 0), (1, 32, 1, 0), (1, 128, 1, 0), (0, 64, 0, 0), (0, 16, 1, 1)):
+        if f % max(hn, 1):
+            continue
+        p = params(fp4, elem, hn, ceil, sr, seed=m * 7 + f)
+        full = layer.gated(aq, w, out_dtype=torch.float32, out_q=p, keep_gu=True)
+        check_products(fp4, aq, gq, uq, act, full, torch.float32)
+        same_codes(full.q, fp4.quantize(full.h, p))
+        got = layer.gated(aq, w, out_q=p, keep_gu=True)
+        same_codes(got.q, full.q)
+        assert torch.equal(got.h, full.h.bfloat16()) and torch.equal(got.gu, full.gu.bfloat16())
+        only = layer.gated(aq, w, out_q=p, keep_h=False, q_out=fp4.empty_qtensor(m, f, p, "cuda"))
+        assert only.h is None and only.gu is None
+        same_codes(only.q, full.q)
+
+
+# ---- calls larger than the caches ----
+
+@pytest.mark.parametrize("elem,tile", [(0, False), (0, True), (1, False)])
+@pytest.mark.parametrize("dtype,m", [(torch.bfloat16, 4096), (torch.float32, 2111)])
+def test_gated_past_the_caches(fp4, layer, dtype, m, elem, tile):
+    """h of 64 MiB and more: stored past the caches, the same bits as those of fewer rows."""
+    f, k, few = 8448, 256, 1024
+    assert m * f * (2 if dtype is torch.bfloat16 else 4) >= 64 << 20 > few * f * 4
+    aq, gq, uq = operands(fp4, gen(m), m, f, k, elem, tile)
+    w = layer.GatedWeights(gq, uq)
+    assert layer.gated_plan(m, w).kernel == layer.gated_plan(few, w).kernel == layer.PLAN_TILE256
+    got = layer.gated(aq, w, out_dtype=dtype, keep_gu=True)
+    check_products(fp4, aq, gq, uq, 0, got, dtype)
+    cb, sb = aq.codes.numel() // m, aq.scales.numel() // m
+    head = fp4.QTensor(aq.codes[:few * cb], aq.scales[:few * sb], None, few, k, aq.params)
+    part = layer.gated(head, w, out_dtype=dtype, keep_gu=True)
+    assert torch.equal(got.h[:few], part.h) and torch.equal(got.gu[:few], part.gu)
+    assert torch.equal(layer.gated(aq, w, out_dtype=dtype).h, got.h)
+    p = params(fp4, 1, 128, 1, 0)
+    coded = layer.gated(aq, w, out_dtype=dtype, out_q=p)
+    assert torch.equal(coded.h, got.h)
+    same_codes(coded.q, fp4.quantize(layer.gated(aq, w, out_dtype=torch.float32).h, p))
+
+
+def slope64(g, act):
+    """The slope and the sum of its terms' magnitudes, without cancellation, and the exponent."""
+    if act == 1:
+        p, rest, z = 0.5 * torch.special.erfc(-g * math.sqrt(0.5)), g * torch.exp(-0.5 * g * g) / math.sqrt(2.0 * math.pi), 0.05 * g * g
+    else:
+        a, b = (1.0, 0.0) if act == 0 else (2.0 * math.sqrt(2.0 / math.pi), 2.0 * math.sqrt(2.0 / math.pi) * 0.044715)
+        z = g * (a + b * g * g)
+        p, rest = torch.sigmoid(z), g * torch.sigmoid(z) * torch.sigmoid(-z) * (a + 3.0 * b * g * g)
+        z = (0.1 if act == 0 else 8.1) * z.abs()
+    return p + rest, p + rest.abs(), z
+
+
+@pytest.mark.parametrize("act", [0, 1, 2])
+def test_gated_backward_past_the_caches(fp4, layer, act):
+    """96 MiB and more of bf16: read and stored past the caches, kept, in place and coded; the same bits as fewer rows."""
+    rows, f, few = 1601, 11008, 130
+    assert rows * f * 6 >= 96 << 20 > few * f * 6
+    g = gen(rows)
+    dh, gu = rand(g, rows, f, dtype=torch.bfloat16), rand(g, rows, 2 * f, size=3.0, dtype=torch.bfloat16)
+    got = layer.gated_backward(dh, gu, act=act)
+    d, gv, uv = dh.double(), gu[:, :f].double(), gu[:, f:].double()
+    half = HALF_STEP[torch.bfloat16]
+    slope, size, z = slope64(gv, act)
+    # where p is below 2^-126 it may vanish, and with it p (1 + |g| z'): z' is at most 1 + |g| + g^2, so that the factor
+    # is below (1 + |g|)^3 (at -10 the third activation's slope is 2e-36 and p 1e-38)
+    tol = ((26.0 + z.clamp(max=900.0)) * E24 * size + (1.0 + gv.abs()) ** 3 * 2.0 ** -125) * (d * uv).abs()
+    near(got.dgu[:, :f], d * uv * slope, tol + half * (d * uv * slope).abs() + 1e-36, "dg")
+    v = d * act64(gv, act)
+    near(got.dgu[:, f:], v, act_bound(gv, act) * d.abs() + half * v.abs() + 1e-36, "du")
+    part = layer.gated_backward(dh[:few], gu[:few], act=act)
+    assert torch.equal(got.dgu[:few], part.dgu)
+    for elem, hn, ceil, sr in ((1, 128, 1, 0), (0, 256, 0, 1)):
+        p = params(fp4, elem, hn, ceil, sr)
+        full = layer.gated_backward(dh.float(), gu.float(), act=act, out_q=p)
+        same_codes(full.q, fp4.quantize(full.dgu, p))
+        coded = layer.gated_backward(dh, gu, act=act, out_q=p)
+        same_codes(coded.q, full.q)
+        assert torch.equal(coded.dgu, got.dgu)
+        same_codes(layer.gated_backward(dh, gu, act=act, out_q=p, keep=False).q, full.q)
+    same = gu.clone()
+    assert torch.equal(layer.gated_backward(dh, same, act=act, out=same).dgu, got.dgu)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype,tokens,dim,rot", [(torch.bfloat16, 7001, 128, 128), (torch.float32, 3501, 128, 64),
+                                                  (torch.bfloat16, 4801, 192, 128), (torch.bfloat16, 11201, 80, 80)])
+def test_rope_past_the_caches(layer, dtype, tokens, dim, rot, interleaved):
+    """64 MiB and more, in whole cache lines and not: pairs, in place, the same bits as few tokens."""
+    hq, hk = 32, 8
+    assert tokens * (hq + hk) * dim * (2 if dtype is torch.bfloat16 else 4) >= 64 << 20
+    g = gen(tokens)
+    fused = rand(g, tokens, hq + 2 * hk, dim, dtype=dtype)
+    q, k = fused[:, :hq], fused[:, hq:hq + hk]
+    f = layer.rotary_frequencies(rot)[0]
+    rotary = layer.Rotary(f.cuda(), layout=layer.INTERLEAVED if interleaved else layer.HALF)
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda") * 100
+    for backward in (False, True):
+        got = layer.rope((q, k), rotary, pos, backward=backward)
+        for x, y in zip((q, k), got):
+            want, size = rope64(x, pos, f.cuda(), interleaved, backward)
+            near(y, want, size * (2.0 ** -22 + 3 * E24 + HALF_STEP[dtype]), "rope")
+            assert torch.equal(y[..., rot:], x[..., rot:])
+        few = layer.rope((q[-31:], k[-31:]), rotary, pos[-31:], backward=backward)
+        assert torch.equal(got[0][-31:], few[0]) and torch.equal(got[1][-31:], few[1])
+    a = fused.clone()
+    layer.rope((a[:, :hq], a[:, hq:hq + hk]), rotary, pos, out=(a[:, :hq], a[:, hq:hq + hk]), backward=True)
+    assert torch.equal(a[:, :hq], got[0]) and torch.equal(a[:, hq:hq + hk], got[1]) and torch.equal(a[:, hq + hk:], fused[:, hq + hk:])
