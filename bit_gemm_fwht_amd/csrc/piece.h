@@ -180,11 +180,13 @@ __device__ __forceinline__ float exp_minus(float y) {
 }
 
 // p = 1 / (1 + e^-x) and its derivative p (1 - p), both to a few roundings of themselves: with e = e^-|x| <= 1 they
-// come from 1 / (1 + e) and e / (1 + e), whose divisor lies in [1, 2] (the hardware's reciprocal: an ulp).
+// come from r = 1 / (1 + e) and s = e r, whose divisor lies in [1, 2] (the hardware's reciprocal: an ulp). p of positive
+// x is 1 - s, whose error is a share of the smaller of the two (root mean square of normal arguments of size 1.5: 0.58
+// half steps, with r 0.78; the exact exponential and quotient 0.68).
 __device__ __forceinline__ float sigmoid(float x, float& slope) {
     const float e = exp_minus(fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e), s = e * r;
     slope = r * s;
-    return x < 0.0f ? s : r;
+    return x < 0.0f ? s : 1.0f - s;
 }
 
 // Phi(g) of the normal distribution, and e = e^(-g^2 / 2), both to a few roundings of themselves: (1 + erf(g / sqrt 2))

@@ -3,8 +3,9 @@
 Bounds are counted in E24 = 2^-24, half a step of fp32 relative to the value; the hardware's exponential and reciprocal
 are off by an ulp, 2 E24 at most.
 - e^-y: exponential 2, its correction 1, and 1.4427 y times the 2^-29 by which ln 2 in fp32 is off: 0.05 y. With
-  e <= 1 the sum 1 + e is off by 1 + 3 / 2, its reciprocal by 2 more, and e times that by 3 + 1: p and 1 - p are off by
-  8.5 at most, g p by 9.5: VALUE = 10, + 0.05 |z|.
+  e <= 1 the sum 1 + e is off by 1 + 3 / 2, its reciprocal by 2 more, and s, e times that, by 3 + 1: 8.5 at most, g s
+  by 9.5: VALUE = 10, + 0.05 |z|. 1 - s is off by less: the exponential's 3 enter s = e / (1 + e) by their share 1 / (1 +
+  e) alone, which leaves 4 + 1.5 where s is 1 / 2 and less of 1 - s where it is smaller, and a rounding.
 - the tanh form's argument z = g (A + B g^2) is off by 4 roundings (square, constants, sum, product), which p passes on
   times |z| (its derivative is p (1 - p) z relative to p): + 4 |z|.
 - slopes are p + g p (1 - p) z'(g): each term's factors and products, of the sum of the terms' magnitudes: 2 * 8.5, four
