@@ -505,8 +505,8 @@ int fp4_rope(const fp4_rope_args* a, void* stream);
  * where K % 128 == 0. Pitches need not be multiples of 16 bytes (that only narrows the stores).
  * act: x / (1 + e^-x); x Phi(x) with the error function; the same with
  * Phi(x) ~ (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2.
- * The first is off by at most 10 half steps of fp32 (2^-24 of the value; 15 below -87), the second by 17 (22), the
- * third by 10 and 4 |z| more, z twice the argument of tanh; values below |x| 2^-125 may vanish.
+ * The first is off by at most 10 half steps of fp32 (2^-24 of the value), 15 towards x = -87; the second by 17, 22
+ * towards -13; the third by 10 and 4 |z| more, z twice the argument of tanh. Values below |x| 2^-125 may vanish.
  * g and u of E4M3 operands carry what the FP8 matrix core drops, as fp4_gemm's results do: of each 8 products
  * what lies 13 bits below the largest.
  * How the work is tiled changes the order of the sums, never what is meant. workspace:
